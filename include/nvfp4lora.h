@@ -245,10 +245,12 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_quantize(
     uint8_t* codes, uint8_t* scales, int64_t scales_bytes,
     nvfp4lora_stream stream);
 
-/* Element types of the routed-MoE LoRA delta's activation, banks and output. */
+/* Element types.  The routed-MoE LoRA delta's activation, banks and output are bf16 or fp16; the
+ * routed-token, norm and quantizer calls and the 8-bit product's output take fp32 too. */
 typedef enum nvfp4lora_dtype {
     NVFP4LORA_DTYPE_BF16 = 0,
-    NVFP4LORA_DTYPE_FP16 = 1
+    NVFP4LORA_DTYPE_FP16 = 1,
+    NVFP4LORA_DTYPE_FP32 = 2
 } nvfp4lora_dtype;
 
 /*
@@ -290,6 +292,121 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_bgmv_moe_gemm2_lora_delta(
     int64_t rank, int64_t hidden_size,
     int32_t lora_dtype, float scale, int32_t out_dtype,
     void* out, nvfp4lora_stream stream);
+
+/*
+ * Routed tokens, sorted by expert: the producer of the grouped call's a rows and m_indptr and of the
+ * LoRA delta's expanded_idx_to_permuted_idx.  Slot i = t * top_k + j of expert e = topk_ids[t, j] is
+ * active when 0 <= e < num_experts; a negative id is an inactive slot.  With c[e] active slots of
+ * expert e:
+ *     m_indptr[0] = 0;  m_indptr[e+1] = m_indptr[e] + align * ceil(c[e] / align)
+ *     row(i) = m_indptr[e] + the number of earlier active slots of e   (slot order)
+ *     rows[row(i)] = x[t];  expanded_idx_to_permuted_idx[i] = row(i), -1 for an inactive slot;
+ *     permuted_idx_to_expanded_idx[row(i)] = i, -1 for every other row of the padded_rows.
+ * Padding rows (inside a segment, of no slot) are written as zeros, or left as they were with
+ * zero_padding == 0; rows from m_indptr[num_experts] on are left as they were.
+ *   x        [num_tokens] rows of row_bytes bytes, contiguous; any element type (rows are copied).
+ *   topk_ids int32 [num_tokens, top_k]; an expert may occur twice in a token's list.
+ *   rows     [padded_rows] rows of row_bytes bytes; padded_rows must hold any routing of these sizes:
+ *            floor((n + min(num_experts, n) * (align - 1)) / align) * align with n = num_tokens * top_k.
+ *   m_indptr int32 [num_experts + 1]; expanded_idx_to_permuted_idx int32 [num_tokens * top_k];
+ *   permuted_idx_to_expanded_idx int32 [padded_rows].
+ *   workspace  4 * 64 * num_experts bytes when num_tokens * top_k > 16384 (else ignored, may be NULL);
+ *            its contents need not be kept; two calls that may run at once need two.
+ * Rules: 1 <= top_k <= 16, 1 <= num_experts <= 1024, 1 <= align <= 4096, num_tokens >= 0 (0 writes an
+ * all-zero m_indptr and -1 entries).  Read on the device only: graph-capturable.  An expert id
+ * >= num_experts is an inactive slot, and the next nvfp4lora_device_status returns
+ * NVFP4LORA_ERR_INVALID_ARG.  The pages have no counterpart.
+ */
+NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_permute(
+    const void* x, int64_t num_tokens, int64_t row_bytes,
+    const int32_t* topk_ids, int64_t top_k, int64_t num_experts, int64_t align, int32_t zero_padding,
+    void* rows, int64_t padded_rows, int32_t* m_indptr,
+    int32_t* expanded_idx_to_permuted_idx, int32_t* permuted_idx_to_expanded_idx,
+    void* workspace, int64_t workspace_bytes, nvfp4lora_stream stream);
+
+/*
+ * Routed tokens, back: out[t] = sum_j topk_weights[t, j] * y[expanded_idx_to_permuted_idx[t, j]] over
+ * the token's slots with an index >= 0 (zero when there is none), in fp32 in slot order, rounded once
+ * to the rows' type.  topk_weights NULL: all weights 1.
+ *   y [padded_rows, H], out [num_tokens, H] of `dtype` (bf16, fp16 or fp32), contiguous, aligned to
+ *   their elements; expanded_idx_to_permuted_idx int32 and topk_weights fp32 [num_tokens, top_k].
+ * An index >= padded_rows is left out, and the next nvfp4lora_device_status returns
+ * NVFP4LORA_ERR_INVALID_ARG.  1 <= top_k <= 16, 1 <= H <= 2^20; num_tokens == 0 enqueues nothing.
+ */
+NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_unpermute(
+    const void* y, int64_t padded_rows, int64_t H, int32_t dtype,
+    const int32_t* expanded_idx_to_permuted_idx, const float* topk_weights,
+    int64_t num_tokens, int64_t top_k, void* out, nvfp4lora_stream stream);
+
+/* Gradient of nvfp4lora_moe_permute by x: grad_x[t] = sum_j grad_rows[row(t, j)] (padding rows' gradients
+ * are not read).  Arguments as for nvfp4lora_moe_unpermute without weights. */
+NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_permute_backward(
+    const void* grad_rows, int64_t padded_rows, int64_t H, int32_t dtype,
+    const int32_t* expanded_idx_to_permuted_idx, int64_t num_tokens, int64_t top_k,
+    void* grad_x, nvfp4lora_stream stream);
+
+/*
+ * Gradients of nvfp4lora_moe_unpermute:
+ *     grad_rows[row(t, j)] = topk_weights[t, j] * grad_out[t]      (rounded once)
+ *     grad_weights[t, j]   = sum_h grad_out[t, h] * y[row(t, j), h] (fp32; 0 for an inactive slot)
+ * Padding rows of the segments get zeros; rows from m_indptr[num_experts] on are left as they were.
+ * The tables are those that nvfp4lora_moe_permute wrote.  topk_weights and grad_weights may both be
+ * NULL (weights 1; y is then not read and may be NULL).  Rules as for nvfp4lora_moe_unpermute.
+ */
+NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_unpermute_backward(
+    const void* grad_out, const void* y, int64_t padded_rows, int64_t H, int32_t dtype,
+    const int32_t* expanded_idx_to_permuted_idx, const int32_t* permuted_idx_to_expanded_idx,
+    const int32_t* m_indptr, int64_t num_experts, const float* topk_weights,
+    int64_t num_tokens, int64_t top_k, void* grad_rows, float* grad_weights, nvfp4lora_stream stream);
+
+/*
+ * 8-bit quantizer: the producer of nvfp4lora_mm_fp8's operands.  Per 1 x 128 group of a row
+ * (block_rows = 1: activations) or 128 x 128 block (block_rows = 128: weights), in fp32:
+ *     amax = max(max |x|, 2^-100);  scale = amax / 448;  q = E4M3(rne)(x * (448 / amax)),
+ * so value(q) * scale approximates x.  The last group of a row, and the last block, may be partial.
+ *   x       [rows, H] of `dtype` (bf16, fp16 or fp32), contiguous, aligned to its elements.
+ *           Finite values: a NaN stays a NaN and an infinity makes its group's scale infinite.
+ *   q       uint8 [rows, H]: E4M3 bytes.
+ *   scales  fp32 [ceil(rows / block_rows), ceil(H / 128)], element (r, g) at
+ *           r * scale_stride_row + g * scale_stride_group (row-major or column-major, no overlap).
+ * rows >= 1, 1 <= H <= 2^20.  The pages have no counterpart.
+ */
+NVFP4LORA_API nvfp4lora_status nvfp4lora_fp8_quantize(
+    const void* x, int64_t rows, int64_t H, int32_t dtype, int64_t block_rows,
+    uint8_t* q, float* scales, int64_t scale_stride_row, int64_t scale_stride_group,
+    nvfp4lora_stream stream);
+
+/*
+ * Residual addition, root-mean-square norm and 8-bit quantization in one pass, in fp32:
+ *     h = x + residual;  residual <- round(h) (in place);
+ *     y = h * (1 / sqrt(mean(h^2) + eps)) * weight;  norm_out <- round(y);
+ *     (q, scales) as nvfp4lora_fp8_quantize with block_rows = 1 gives them for the unrounded y.
+ * residual NULL: h = x, nothing is written back.  norm_out NULL: not written.  x, residual, weight [H]
+ * and norm_out have one type `dtype`; x and norm_out may be the same buffer.
+ */
+NVFP4LORA_API nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(
+    const void* x, void* residual, const void* weight, int64_t rows, int64_t H, int32_t dtype, float eps,
+    void* norm_out, uint8_t* q, float* scales, int64_t scale_stride_row, int64_t scale_stride_group,
+    nvfp4lora_stream stream);
+
+/*
+ * 8-bit product with a scale for each block of 128:
+ *     out[m, n] = round( sum_kb a_scale[m, kb] * b_scale[n / 128, kb]
+ *                               * (sum over the columns k of block kb of a[m, k] * b[n, k])  [+ bias[n]] )
+ *   a       uint8 [M, K] E4M3 bytes, row-major; b uint8 [N, K] (the product is a @ b^T).
+ *   a_scale fp32, element (m, kb) at m * a_scale_stride_m + kb * a_scale_stride_k, kb < ceil(K / 128)
+ *           (non-negative strides; 0 repeats a value).  Consecutive m next to each other is fastest.
+ *   b_scale fp32 [ceil(N / 128), ceil(K / 128)] row-major.
+ *   bias    bf16 [N] or NULL, added in fp32 before the single rounding.
+ *   out     out_dtype (bf16, fp16 or fp32) [M, N] row-major, aligned to its elements.
+ * Sums are held in fp32.  Rules: M >= 1, N >= 1, K >= 16 with K % 16 == 0 (K <= 2^20); a and b 16-byte
+ * aligned.  The last K block and the last 128 rows of b may be partial.  The pages have no counterpart.
+ */
+NVFP4LORA_API nvfp4lora_status nvfp4lora_mm_fp8(
+    const uint8_t* a, const uint8_t* b,
+    const float* a_scale, int64_t a_scale_stride_m, int64_t a_scale_stride_k, const float* b_scale,
+    const uint16_t* bias, void* out, int32_t out_dtype,
+    int64_t M, int64_t N, int64_t K, nvfp4lora_stream stream);
 
 /* Message of the last failing call on this host thread ("" when none). */
 NVFP4LORA_API const char* nvfp4lora_last_error(void);

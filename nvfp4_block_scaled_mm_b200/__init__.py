@@ -16,14 +16,16 @@ Two layers:
   ``StaleAdapterError`` -- the API of flashinfer.gemm.mm_nvfp4_lora and
   flashinfer.gemm.prepare_nvfp4_lora_adapter (signatures, Parameters, Returns, Notes);
   ``grouped_mm_nvfp4_lora`` (grouped_mm_bf16's grouped form), ``fp4_quantize``, and
-  ``bgmv_moe_gemm2_lora_delta`` / ``fill_w_ptr`` (flashinfer.fused_moe.bgmv_moe_gemm2_lora_delta).
+  ``bgmv_moe_gemm2_lora_delta`` / ``fill_w_ptr`` (flashinfer.fused_moe.bgmv_moe_gemm2_lora_delta);
+* ``moe_permute`` / ``moe_unpermute`` (the grouped call's rows and tables, and back, with gradients),
+  ``add_rmsnorm_fp8_quantize``, ``fp8_quantize`` and ``mm_fp8`` (the 8-bit layers beside the NVFP4 ones).
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -35,6 +37,10 @@ __all__ = [
     "nvfp4lora_device_status", "nvfp4lora_quantize", "fp4_quantize", "library_path", "version",
     "nvfp4lora_grouped_mm", "grouped_mm_nvfp4_lora", "nvfp4lora_bgmv_moe_gemm2_lora_delta",
     "bgmv_moe_gemm2_lora_delta", "fill_w_ptr",
+    "MoePermutation", "moe_capacity", "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+    "fp8_quantize", "add_rmsnorm_fp8_quantize", "mm_fp8",
+    "nvfp4lora_moe_permute", "nvfp4lora_moe_permute_backward", "nvfp4lora_moe_unpermute",
+    "nvfp4lora_moe_unpermute_backward", "nvfp4lora_fp8_quantize", "nvfp4lora_rmsnorm_fp8_quantize", "nvfp4lora_mm_fp8",
 ]
 
 OK, INVALID_ARG, STALE, ALPHA_ZERO, UNSUPPORTED_ARCH, DEVICE_TIMEOUT, CUDA_ERR = range(7)
@@ -74,11 +80,24 @@ def _load():
     lib.nvfp4lora_bgmv_moe_gemm2_lora_delta.argtypes = [P, I64, I64, P, P, I64, P, I64, P, P, P, I64, I64, I64, I64,
                                                         I64, ctypes.c_int32, ctypes.c_float, ctypes.c_int32, P, P]
     lib.nvfp4lora_bgmv_moe_gemm2_lora_delta.restype = ctypes.c_int
+    lib.nvfp4lora_moe_permute.argtypes = [P, I64, I64, P, I64, I64, I64, I32, P, I64, P, P, P, P, I64, P]
+    lib.nvfp4lora_moe_permute.restype = ctypes.c_int
+    lib.nvfp4lora_moe_unpermute.argtypes = [P, I64, I64, I32, P, P, I64, I64, P, P]
+    lib.nvfp4lora_moe_unpermute.restype = ctypes.c_int
+    lib.nvfp4lora_moe_permute_backward.argtypes = [P, I64, I64, I32, P, I64, I64, P, P]
+    lib.nvfp4lora_moe_permute_backward.restype = ctypes.c_int
+    lib.nvfp4lora_moe_unpermute_backward.argtypes = [P, P, I64, I64, I32, P, P, P, I64, P, I64, I64, P, P, P]
+    lib.nvfp4lora_moe_unpermute_backward.restype = ctypes.c_int
+    lib.nvfp4lora_fp8_quantize.argtypes = [P, I64, I64, I32, I64, P, P, I64, I64, P]
+    lib.nvfp4lora_fp8_quantize.restype = ctypes.c_int
+    lib.nvfp4lora_rmsnorm_fp8_quantize.argtypes = [P, P, P, I64, I64, I32, ctypes.c_float, P, P, P, I64, I64, P]
+    lib.nvfp4lora_rmsnorm_fp8_quantize.restype = ctypes.c_int
+    lib.nvfp4lora_mm_fp8.argtypes = [P, P, P, I64, I64, P, P, P, I32, I64, I64, I64, P]
+    lib.nvfp4lora_mm_fp8.restype = ctypes.c_int
     lib.nvfp4lora_last_error.argtypes = []
     lib.nvfp4lora_last_error.restype = ctypes.c_char_p
     lib.nvfp4lora_version.argtypes = []
     lib.nvfp4lora_version.restype = ctypes.c_char_p
-    del I32
     return lib
 
 
@@ -198,9 +217,68 @@ def nvfp4lora_bgmv_moe_gemm2_lora_delta(act, padded_rows, I, perm, w_ptr_a, lora
     return out
 
 
+def nvfp4lora_moe_permute(x, num_tokens, row_bytes, topk_ids, top_k, num_experts, align, zero_padding, rows,
+                          padded_rows, m_indptr, expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx,
+                          workspace=None, workspace_bytes=0, stream=None):
+    _check(_lib.nvfp4lora_moe_permute(_ptr(x), int(num_tokens), int(row_bytes), _ptr(topk_ids), int(top_k),
+                                      int(num_experts), int(align), int(bool(zero_padding)), _ptr(rows),
+                                      int(padded_rows), _ptr(m_indptr), _ptr(expanded_idx_to_permuted_idx),
+                                      _ptr(permuted_idx_to_expanded_idx), _ptr(workspace), int(workspace_bytes),
+                                      _stream(stream)))
+    return rows
+
+
+def nvfp4lora_moe_unpermute(y, padded_rows, H, dtype, expanded_idx_to_permuted_idx, topk_weights, num_tokens, top_k,
+                            out, stream=None):
+    _check(_lib.nvfp4lora_moe_unpermute(_ptr(y), int(padded_rows), int(H), int(dtype),
+                                        _ptr(expanded_idx_to_permuted_idx), _ptr(topk_weights), int(num_tokens),
+                                        int(top_k), _ptr(out), _stream(stream)))
+    return out
+
+
+def nvfp4lora_moe_permute_backward(grad_rows, padded_rows, H, dtype, expanded_idx_to_permuted_idx, num_tokens, top_k,
+                                   grad_x, stream=None):
+    _check(_lib.nvfp4lora_moe_permute_backward(_ptr(grad_rows), int(padded_rows), int(H), int(dtype),
+                                               _ptr(expanded_idx_to_permuted_idx), int(num_tokens), int(top_k),
+                                               _ptr(grad_x), _stream(stream)))
+    return grad_x
+
+
+def nvfp4lora_moe_unpermute_backward(grad_out, y, padded_rows, H, dtype, expanded_idx_to_permuted_idx,
+                                     permuted_idx_to_expanded_idx, m_indptr, num_experts, topk_weights, num_tokens,
+                                     top_k, grad_rows, grad_weights, stream=None):
+    _check(_lib.nvfp4lora_moe_unpermute_backward(
+        _ptr(grad_out), _ptr(y), int(padded_rows), int(H), int(dtype), _ptr(expanded_idx_to_permuted_idx),
+        _ptr(permuted_idx_to_expanded_idx), _ptr(m_indptr), int(num_experts), _ptr(topk_weights), int(num_tokens),
+        int(top_k), _ptr(grad_rows), _ptr(grad_weights), _stream(stream)))
+    return grad_rows, grad_weights
+
+
+def nvfp4lora_fp8_quantize(x, rows, H, dtype, block_rows, q, scales, scale_stride_row, scale_stride_group, stream=None):
+    _check(_lib.nvfp4lora_fp8_quantize(_ptr(x), int(rows), int(H), int(dtype), int(block_rows), _ptr(q), _ptr(scales),
+                                       int(scale_stride_row), int(scale_stride_group), _stream(stream)))
+    return q, scales
+
+
+def nvfp4lora_rmsnorm_fp8_quantize(x, residual, weight, rows, H, dtype, eps, norm_out, q, scales, scale_stride_row,
+                                   scale_stride_group, stream=None):
+    _check(_lib.nvfp4lora_rmsnorm_fp8_quantize(_ptr(x), _ptr(residual), _ptr(weight), int(rows), int(H), int(dtype),
+                                               float(eps), _ptr(norm_out), _ptr(q), _ptr(scales),
+                                               int(scale_stride_row), int(scale_stride_group), _stream(stream)))
+    return q, scales
+
+
+def nvfp4lora_mm_fp8(a, b, a_scale, a_scale_stride_m, a_scale_stride_k, b_scale, bias, out, out_dtype, M, N, K,
+                     stream=None):
+    _check(_lib.nvfp4lora_mm_fp8(_ptr(a), _ptr(b), _ptr(a_scale), int(a_scale_stride_m), int(a_scale_stride_k),
+                                 _ptr(b_scale), _ptr(bias), _ptr(out), int(out_dtype), int(M), int(N), int(K),
+                                 _stream(stream)))
+    return out
+
+
 def nvfp4lora_device_status(stream=None) -> None:
     """Synchronise the stream; raise DeviceTimeoutError if a kernel's wait ran out, ValueError if a
-    table read on the device (a grouped call's m_indptr, a LoRA delta's routing) broke its rules."""
+    table read on the device (a grouped call's m_indptr, a LoRA delta's or a permutation's routing) broke its rules."""
     _check(_lib.nvfp4lora_device_status(_stream(stream)))
 
 
@@ -549,3 +627,380 @@ def fp4_quantize(x: torch.Tensor, global_scale: torch.Tensor, *, codes: Optional
     with torch.cuda.device(x.device):
         nvfp4lora_quantize(x, rows, K, global_scale, codes, scales, torch.cuda.current_stream(x.device))
     return codes, scales
+
+# --------------------------------------------------------------------------------------
+# routed tokens: rows sorted by expert for the grouped call, and back
+# --------------------------------------------------------------------------------------
+
+_ROW_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_SELF_COUNT_SLOTS = 16384      # more slots than this take a workspace
+_COUNT_CHUNKS = 64
+
+
+class _Here:
+    """Stands in for ``torch.cuda.device`` where the tensors' device is the current one already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on_device(device: torch.device):
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+class MoePermutation(NamedTuple):
+    """Routed tokens sorted by expert (:func:`moe_permute`): ``rows [capacity, H]``, ``m_indptr``
+    int32 ``[E + 1]`` (the grouped call's), ``expanded_idx_to_permuted_idx`` int32 ``[T, top_k]``
+    (the LoRA delta's; -1 for an inactive slot) and ``permuted_idx_to_expanded_idx`` int32
+    ``[capacity]`` (-1 for rows of no slot)."""
+
+    rows: torch.Tensor
+    m_indptr: torch.Tensor
+    expanded_idx_to_permuted_idx: torch.Tensor
+    permuted_idx_to_expanded_idx: torch.Tensor
+
+
+def moe_capacity(num_tokens: int, top_k: int, num_experts: int, align: int = 128) -> int:
+    """The rows that any routing of ``num_tokens`` tokens to ``top_k`` of ``num_experts`` experts can
+    need with segments of multiples of ``align`` rows."""
+    n = num_tokens * top_k
+    return (n + min(num_experts, n) * (align - 1)) // align * align
+
+
+def _need_row_dtype(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ROW_DTYPES:
+        raise ValueError(f"{name} must be a torch.bfloat16, torch.float16 or torch.float32 tensor")
+
+
+def _moe_permute(x, topk_ids, num_experts, align, zero_padding, out):
+    T, top_k = topk_ids.shape
+    dev = x.device
+    capacity = out.shape[0]
+    with _on_device(dev):
+        n = T * top_k
+        # one allocation for the tables; the row -> slot table starts on a 16-byte boundary
+        a, b = -(-(num_experts + 1) // 4) * 4, -(-n // 4) * 4
+        ws = _COUNT_CHUNKS * num_experts if n > _SELF_COUNT_SLOTS else 0
+        tables = torch.empty(a + b + capacity, dtype=torch.int32, device=dev)
+        m_indptr = tables[:num_experts + 1]
+        idx = tables[a:a + n].view(T, top_k)
+        inv = tables[a + b:]
+        work = torch.empty(ws, dtype=torch.int32, device=dev) if ws else None
+        nvfp4lora_moe_permute(x, T, x.shape[1] * x.element_size(), topk_ids, top_k, num_experts, align, zero_padding,
+                              out, capacity, m_indptr, idx, inv, work, 4 * ws, torch.cuda.current_stream(dev))
+    return out, m_indptr, idx, inv
+
+
+def _refuse_recording_in_capture(name: str, instead: str) -> None:
+    # The gradient's accumulation nodes of leaves that an eager graph keeps alive belong to the stream
+    # they were made on: running them inside a capture on another stream breaks the capture, and the
+    # process ends with it.
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError(f"{name} of tensors that require gradients does not record a graph while a CUDA graph is being "
+                         f"captured: call it on detached tensors and capture {instead}")
+
+
+class _MoePermuteFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, topk_ids, num_experts, align, zero_padding, out):
+        rows, m_indptr, idx, inv = _moe_permute(x, topk_ids, num_experts, align, zero_padding, out)
+        ctx.save_for_backward(idx)
+        ctx.mark_non_differentiable(m_indptr, idx, inv)
+        return rows, m_indptr, idx, inv
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_rows, *_):
+        (idx,) = ctx.saved_tensors
+        return moe_permute_backward(grad_rows.contiguous(), idx), None, None, None, None, None
+
+
+def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, align: int = 128,
+                zero_padding: bool = True, out: Optional[torch.Tensor] = None) -> MoePermutation:
+    """Sort the rows of routed tokens by expert, for :func:`grouped_mm_nvfp4_lora` (``m_indptr``) and
+    :func:`bgmv_moe_gemm2_lora_delta` (``expanded_idx_to_permuted_idx``).
+
+    x: ``[T, H]`` of any element type, contiguous; topk_ids: int32 ``[T, top_k]`` (negative: an
+    inactive slot; an expert may occur twice).  Expert e's segment holds the rows of its slots in slot
+    order (``t * top_k + j``) and is padded to a multiple of ``align`` rows (128 for the grouped
+    call).  Padding rows are zeros, or left as they were with ``zero_padding=False``; rows from
+    ``m_indptr[E]`` on are left as they were.  ``out``: a ``[capacity, H]`` buffer for the rows with
+    ``capacity >= moe_capacity(T, top_k, E, align)``.  1 <= top_k <= 16, 1 <= E <= 1024.
+
+    Differentiable in x (bf16, fp16, fp32): the gradient is :func:`moe_permute_backward`; padding
+    rows' gradients are not read.  Tensors that require gradients are refused while a CUDA graph is
+    captured (capture the two functions on detached tensors instead).  An id >= num_experts is read
+    on the device: it counts as inactive and :func:`nvfp4lora_device_status` raises ValueError.
+    """
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA tensor of 2 dimensions")
+    _need(topk_ids, "topk_ids", torch.int32, 2)
+    T, top_k = topk_ids.shape
+    E, align = int(num_experts), int(align)
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows but topk_ids {T}")
+    if x.shape[1] < 1:
+        raise ValueError("x must have at least one column")
+    if not 1 <= E <= 1024 or not 1 <= align <= 4096:
+        raise ValueError(f"num_experts = {E}, align = {align}: 1 <= num_experts <= 1024 and 1 <= align <= 4096 are required")
+    capacity = moe_capacity(T, top_k, E, align)
+    record = torch.is_grad_enabled() and x.requires_grad
+    if out is None:
+        out = torch.empty((capacity, x.shape[1]), dtype=x.dtype, device=x.device)
+    else:
+        _need(out, "out", x.dtype, 2)
+        if out.shape[0] < capacity or out.shape[1] != x.shape[1]:
+            raise ValueError(f"out must be [capacity, H] with capacity >= {capacity} and H = {x.shape[1]}, got {tuple(out.shape)}")
+        if record:
+            raise ValueError("out is not supported for an x that requires gradients")
+    _same_device("x", x, topk_ids=topk_ids, out=out)
+    if record:
+        _need_row_dtype(x, "x that requires gradients")
+        _refuse_recording_in_capture("moe_permute", "moe_permute_backward")
+        return MoePermutation(*_MoePermuteFn.apply(x, topk_ids, E, align, zero_padding, out))
+    return MoePermutation(*_moe_permute(x, topk_ids, E, align, zero_padding, out))
+
+
+def moe_permute_backward(grad_rows: torch.Tensor, expanded_idx_to_permuted_idx: torch.Tensor, *,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of :func:`moe_permute` by x: ``grad_x[t] = sum_j grad_rows[idx[t, j]]`` over the active
+    slots, in fp32 in slot order, rounded once."""
+    return _moe_unpermute(grad_rows, expanded_idx_to_permuted_idx, None, out, "grad_rows")
+
+
+def _moe_unpermute(y, idx, topk_weights, out, name="y"):
+    _need_row_dtype(y, name)
+    _need(y, name, y.dtype, 2)
+    _need(idx, "expanded_idx_to_permuted_idx", torch.int32, 2)
+    T, top_k = idx.shape
+    H = y.shape[1]
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, 2)
+        if topk_weights.shape != idx.shape:
+            raise ValueError(f"topk_weights must be [T, top_k] = {tuple(idx.shape)}, got {tuple(topk_weights.shape)}")
+    if out is None:
+        out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+    else:
+        _need(out, "out", y.dtype, 2)
+        if tuple(out.shape) != (T, H):
+            raise ValueError(f"out must be [T, H] = [{T}, {H}], got {tuple(out.shape)}")
+    _same_device(name, y, expanded_idx_to_permuted_idx=idx, topk_weights=topk_weights, out=out)
+    with _on_device(y.device):
+        nvfp4lora_moe_unpermute(y, y.shape[0], H, _ROW_DTYPES[y.dtype], idx, topk_weights, T, top_k, out,
+                                torch.cuda.current_stream(y.device))
+    return out
+
+
+class _MoeUnpermuteFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, topk_weights, m_indptr, idx, inv):
+        ctx.weighted = topk_weights is not None
+        ctx.save_for_backward(y, topk_weights, m_indptr, idx, inv)
+        return _moe_unpermute(y, idx, topk_weights, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        y, w, m_indptr, idx, inv = ctx.saved_tensors
+        # rows behind the last segment get no gradient: their memory is written by no kernel
+        grad_rows = torch.zeros_like(y)
+        gy, gw = moe_unpermute_backward(grad_out.contiguous(), y, idx, inv, m_indptr, w, grad_rows=grad_rows)
+        return gy, gw, None, None, None
+
+
+def moe_unpermute(y: torch.Tensor, permutation, topk_weights: Optional[torch.Tensor] = None, *,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Bring the experts' rows back to their tokens: ``out[t] = sum_j topk_weights[t, j] * y[idx[t, j]]``
+    over the token's active slots (zero without one), in fp32 in slot order, rounded once to y's type.
+
+    y: bf16, fp16 or fp32 ``[rows, H]``; permutation: a :class:`MoePermutation`, or its
+    ``expanded_idx_to_permuted_idx`` (int32 ``[T, top_k]``) alone; topk_weights: fp32 ``[T, top_k]``,
+    None for weights of 1.  An index >= rows is read on the device: it is left out and
+    :func:`nvfp4lora_device_status` raises ValueError.
+
+    Differentiable in y and topk_weights where the whole MoePermutation is given (its gradient,
+    :func:`moe_unpermute_backward`, needs the tables); as for :func:`moe_permute`, not while a CUDA
+    graph is captured.
+    """
+    whole = isinstance(permutation, MoePermutation)
+    idx = permutation.expanded_idx_to_permuted_idx if whole else permutation
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (y, topk_weights)):
+        if not whole:
+            raise ValueError("y or topk_weights requires gradients: pass the MoePermutation, whose tables the gradient needs")
+        if out is not None:
+            raise ValueError("out is not supported for inputs that require gradients")
+        if permutation.permuted_idx_to_expanded_idx.shape[0] != y.shape[0]:
+            raise ValueError(f"y has {y.shape[0]} rows but the permutation {permutation.permuted_idx_to_expanded_idx.shape[0]}")
+        _refuse_recording_in_capture("moe_unpermute", "moe_unpermute_backward")
+        return _MoeUnpermuteFn.apply(y, topk_weights, permutation.m_indptr, idx, permutation.permuted_idx_to_expanded_idx)
+    return _moe_unpermute(y, idx, topk_weights, out)
+
+
+def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], expanded_idx_to_permuted_idx: torch.Tensor,
+                           permuted_idx_to_expanded_idx: torch.Tensor, m_indptr: torch.Tensor,
+                           topk_weights: Optional[torch.Tensor] = None, *, grad_rows: Optional[torch.Tensor] = None):
+    """Gradients of :func:`moe_unpermute`: ``(grad_rows, grad_weights)`` with
+    ``grad_rows[idx[t, j]] = topk_weights[t, j] * grad_out[t]`` and ``grad_weights[t, j] = <grad_out[t],
+    y[idx[t, j]]>`` (fp32; 0 for an inactive slot; None without weights, where y is not read and may be
+    None).  Padding rows of the segments get zeros; rows from ``m_indptr[E]`` on are left as they were
+    in ``grad_rows`` (a ``[rows, H]`` buffer; uninitialised there when None).  The tables are those of
+    one :class:`MoePermutation`."""
+    _need_row_dtype(grad_out, "grad_out")
+    _need(grad_out, "grad_out", grad_out.dtype, 2)
+    idx, inv = expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx
+    _need(idx, "expanded_idx_to_permuted_idx", torch.int32, 2)
+    _need(inv, "permuted_idx_to_expanded_idx", torch.int32, 1)
+    _need(m_indptr, "m_indptr", torch.int32, 1)
+    T, top_k = idx.shape
+    rows, H = inv.shape[0], grad_out.shape[1]
+    if grad_out.shape[0] != T:
+        raise ValueError(f"grad_out has {grad_out.shape[0]} rows but expanded_idx_to_permuted_idx {T}")
+    grad_weights = None
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, 2)
+        if topk_weights.shape != idx.shape:
+            raise ValueError(f"topk_weights must be [T, top_k] = {tuple(idx.shape)}, got {tuple(topk_weights.shape)}")
+        _need(y, "y", grad_out.dtype, 2)
+        if tuple(y.shape) != (rows, H):
+            raise ValueError(f"y must be [rows, H] = [{rows}, {H}], got {tuple(y.shape)}")
+        grad_weights = torch.empty((T, top_k), dtype=torch.float32, device=grad_out.device)
+    if grad_rows is None:
+        grad_rows = torch.empty((rows, H), dtype=grad_out.dtype, device=grad_out.device)
+    else:
+        _need(grad_rows, "grad_rows", grad_out.dtype, 2)
+        if tuple(grad_rows.shape) != (rows, H):
+            raise ValueError(f"grad_rows must be [rows, H] = [{rows}, {H}], got {tuple(grad_rows.shape)}")
+    _same_device("grad_out", grad_out, y=y, expanded_idx_to_permuted_idx=idx, permuted_idx_to_expanded_idx=inv,
+                 m_indptr=m_indptr, topk_weights=topk_weights, grad_rows=grad_rows)
+    with _on_device(grad_out.device):
+        nvfp4lora_moe_unpermute_backward(grad_out, y if topk_weights is not None else None, rows, H,
+                                         _ROW_DTYPES[grad_out.dtype], idx, inv, m_indptr, m_indptr.shape[0] - 1,
+                                         topk_weights, T, top_k, grad_rows, grad_weights,
+                                         torch.cuda.current_stream(grad_out.device))
+    return grad_rows, grad_weights
+
+
+# --------------------------------------------------------------------------------------
+# 8-bit operands and product
+# --------------------------------------------------------------------------------------
+
+def _fp8_outputs(x, block_rows, q, scales):
+    rows, H = x.shape
+    shape = (-(-rows // block_rows), -(-H // 128))
+    if q is None:
+        q = torch.empty((rows, H), dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _need(q, "q", torch.float8_e4m3fn, 2)
+        if tuple(q.shape) != (rows, H):
+            raise ValueError(f"q must be [rows, H] = [{rows}, {H}], got {tuple(q.shape)}")
+    if scales is None:
+        # activations' scales column-major: the product reads consecutive rows' scales together
+        strides = (1, shape[0]) if block_rows == 1 else (shape[1], 1)
+        scales = torch.empty_strided(shape, strides, dtype=torch.float32, device=x.device)
+    elif (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or not scales.is_cuda
+          or tuple(scales.shape) != shape):
+        raise ValueError(f"scales must be a float32 CUDA tensor of shape {shape}")
+    return q, scales
+
+
+def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None):
+    """Quantize ``x [rows, H]`` (bf16, fp16 or fp32) into the operand format of :func:`mm_fp8`:
+    ``q`` float8_e4m3fn ``[rows, H]`` and fp32 ``scales [ceil(rows / block_rows), ceil(H / 128)]``,
+    ``value(q) * scale`` approximating x.  ``block_rows=1``: a scale per 128 values of a row
+    (activations; scales are column-major unless given).  ``block_rows=128``: a scale per 128 x 128
+    block (weights).  Rule, in fp32: ``amax = max(max |x|, 2^-100)``, ``scale = amax / 448``,
+    ``q = e4m3(x * (448 / amax))``, nearest even.  Finite values are expected: a NaN stays a NaN, an
+    infinity makes its group's scale infinite."""
+    _need_row_dtype(x, "x")
+    _need(x, "x", x.dtype, 2)
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows = {block_rows}: 1 or 128 is required")
+    q, scales = _fp8_outputs(x, block_rows, q, scales)
+    _same_device("x", x, q=q, scales=scales)
+    sr, sg = scales.stride()
+    with _on_device(x.device):
+        nvfp4lora_fp8_quantize(x, x.shape[0], x.shape[1], _ROW_DTYPES[x.dtype], block_rows, q, scales, sr, sg,
+                               torch.cuda.current_stream(x.device))
+    return q, scales
+
+
+def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                             eps: float = 1e-6, norm_out: Optional[torch.Tensor] = None,
+                             q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """Residual addition, root-mean-square norm and 8-bit quantization in one pass over ``x [rows, H]``,
+    in fp32: ``h = x + residual`` (``residual`` is updated in place with the rounded h),
+    ``y = h * rsqrt(mean(h^2) + eps) * weight``; returns ``(q, scales)`` of y as :func:`fp8_quantize`
+    with ``block_rows=1`` gives them (from the unrounded y), the ``a`` and ``a_scale`` of
+    :func:`mm_fp8`.  ``norm_out [rows, H]`` also receives y in x's type (a router or a LoRA down
+    projection reads it); it may be x itself.  x, weight ``[H]``, residual and norm_out share one type
+    (bf16, fp16 or fp32).  Not differentiable."""
+    _need_row_dtype(x, "x")
+    _need(x, "x", x.dtype, 2)
+    H = x.shape[1]
+    _need(weight, "weight", x.dtype, 1)
+    if weight.shape[0] != H:
+        raise ValueError(f"weight must be [H] = [{H}], got {tuple(weight.shape)}")
+    for name, t in (("residual", residual), ("norm_out", norm_out)):
+        if t is not None:
+            _need(t, name, x.dtype, 2)
+            if t.shape != x.shape:
+                raise ValueError(f"{name} must be [rows, H] = {tuple(x.shape)}, got {tuple(t.shape)}")
+    q, scales = _fp8_outputs(x, 1, q, scales)
+    _same_device("x", x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
+    sr, sg = scales.stride()
+    with _on_device(x.device):
+        nvfp4lora_rmsnorm_fp8_quantize(x, residual, weight, x.shape[0], H, _ROW_DTYPES[x.dtype], eps, norm_out, q,
+                                       scales, sr, sg, torch.cuda.current_stream(x.device))
+    return q, scales
+
+
+def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: torch.Tensor, *,
+           bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+           out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """``out[m, n] = sum_kb a_scale[m, kb] * b_scale[n // 128, kb] * (a[m, kb block] . b[n, kb block]) [+ bias[n]]``
+    with K blocks of 128, sums in fp32, rounded once to ``out_dtype`` (bf16, fp16 or fp32).
+
+    a: float8_e4m3fn ``[M, K]``; b: float8_e4m3fn ``[N, K]``; a_scale: fp32 ``[M, ceil(K / 128)]`` of any
+    strides (column-major, as :func:`fp8_quantize` makes it, is read fastest); b_scale: fp32
+    ``[ceil(N / 128), ceil(K / 128)]`` contiguous; bias: bf16 ``[N]``.  K % 16 == 0; any M, N >= 1.  As for
+    :func:`mm_nvfp4_lora`, out is defined once a later :func:`nvfp4lora_device_status` has returned
+    without raising ``DeviceTimeoutError``.  Not differentiable."""
+    _need(a, "a", torch.float8_e4m3fn, 2)
+    _need(b, "b", torch.float8_e4m3fn, 2)
+    _need(b_scale, "b_scale", torch.float32, 2)
+    M, K = a.shape
+    N = b.shape[0]
+    G = -(-K // 128)
+    if b.shape[1] != K:
+        raise ValueError(f"a is [M, K] = {tuple(a.shape)} but b is {tuple(b.shape)}: K differs")
+    if not isinstance(a_scale, torch.Tensor) or a_scale.dtype != torch.float32 or not a_scale.is_cuda:
+        raise ValueError("a_scale must be a float32 CUDA tensor")
+    if tuple(a_scale.shape) != (M, G):
+        raise ValueError(f"a_scale must be [M, ceil(K / 128)] = [{M}, {G}], got {tuple(a_scale.shape)}")
+    if tuple(b_scale.shape) != (-(-N // 128), G):
+        raise ValueError(f"b_scale must be [ceil(N / 128), ceil(K / 128)] = [{-(-N // 128)}, {G}], got {tuple(b_scale.shape)}")
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, 1)
+        if bias.shape[0] != N:
+            raise ValueError(f"bias must be [N] = [{N}]")
+    if out_dtype not in _ROW_DTYPES:
+        raise ValueError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    else:
+        _need(out, "out", out_dtype, 2)
+        if tuple(out.shape) != (M, N):
+            raise ValueError(f"out must be [M, N] = [{M}, {N}]")
+    _same_device("a", a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
+    sm, sk = a_scale.stride()
+    with _on_device(a.device):
+        nvfp4lora_mm_fp8(a, b, a_scale, sm, sk, b_scale, bias, out, _ROW_DTYPES[out_dtype], M, N, K,
+                         torch.cuda.current_stream(a.device))
+    return out

@@ -17,16 +17,22 @@
 #include <cstdio>
 #include <cstring>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <set>
 #include <string>
+#include <type_traits>
 
 #include "../../include/nvfp4lora.h"
 #include "bgmv.cuh"
 #include "fold.cuh"
+#include "fp8_gemm.cuh"
+#include "fp8_quant.cuh"
+#include "fp8_splitk.cuh"
 #include "gemm.cuh"
 #include "gemm_decode.cuh"
 #include "gemm_pair.cuh"
+#include "moe.cuh"
 #include "ptx.cuh"
 #include "quantize.cuh"
 #include "selftest.cuh"
@@ -659,6 +665,217 @@ nvfp4lora_status check_fold_args(const uint16_t* lora_b, const float* lora_scale
     return NVFP4LORA_OK;
 }
 
+// ---------------------------------------------------------------------------------------
+// routed tokens, 8-bit quantizers and the 8-bit product: shared launch helpers
+// ---------------------------------------------------------------------------------------
+
+// A launch with the programmatic serialization attribute: every kernel launched through it waits
+// (griddepcontrol.wait) before it touches memory that an earlier kernel may write.
+template <typename Kernel, typename... Args>
+nvfp4lora_status launch_dependent(const char* what, Kernel kernel, int64_t grid, int block, cudaStream_t stream,
+                                  const Args&... kargs) {
+    if (grid > INT32_MAX) return fail(NVFP4LORA_ERR_INVALID_ARG, "%s: too large (more than 2^31 blocks)", what);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, kargs...);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    return NVFP4LORA_OK;
+}
+
+// Slots up to which every CTA of the permute kernel counts all of them itself (one launch).
+constexpr int64_t kMoeSelfCountSlots = 16384;
+
+nvfp4lora_status check_routing(int64_t T, int64_t top_k, int64_t rows) {
+    if (T < 0 || T > kMaxDim) return fail(NVFP4LORA_ERR_INVALID_ARG, "num_tokens = %lld out of range", (long long)T);
+    if (top_k < 1 || top_k > kMoeMaxTopK)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "top_k = %lld: 1 <= top_k <= %d is required", (long long)top_k, kMoeMaxTopK);
+    if (T * top_k > kMaxDim) return fail(NVFP4LORA_ERR_INVALID_ARG, "num_tokens * top_k too large");
+    if (rows < 0 || rows > kMaxDim) return fail(NVFP4LORA_ERR_INVALID_ARG, "padded_rows = %lld out of range", (long long)rows);
+    return NVFP4LORA_OK;
+}
+
+bool valid_type(int32_t t) {
+    return t == NVFP4LORA_DTYPE_BF16 || t == NVFP4LORA_DTYPE_FP16 || t == NVFP4LORA_DTYPE_FP32;
+}
+
+int type_bytes(int32_t t) { return t == NVFP4LORA_DTYPE_FP32 ? 4 : 2; }
+
+// The element type of a row operator as a template argument.
+template <typename F>
+nvfp4lora_status by_type(int32_t t, F f) {
+    if (t == NVFP4LORA_DTYPE_BF16) return f(std::integral_constant<MoeType, MoeType::BF16>{});
+    if (t == NVFP4LORA_DTYPE_FP16) return f(std::integral_constant<MoeType, MoeType::FP16>{});
+    return f(std::integral_constant<MoeType, MoeType::FP32>{});
+}
+
+bool rows_aligned16(int64_t row_bytes, std::initializer_list<const void*> ptrs) {
+    if (row_bytes % 16 != 0) return false;
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return false;
+    return true;
+}
+
+nvfp4lora_status check_scale_strides(int64_t rows, int64_t groups, int64_t sr, int64_t sg) {
+    // an output: no two elements may share an address
+    const bool row_major = sg >= 1 && (rows <= 1 || sr >= (groups - 1) * sg + 1);
+    const bool col_major = sr >= 1 && (groups <= 1 || sg >= (rows - 1) * sr + 1);
+    if (!(row_major || col_major) || sr < 0 || sg < 0)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "scales strides (%lld, %lld): row-major or column-major elements that do "
+                    "not overlap are required", (long long)sr, (long long)sg);
+    return NVFP4LORA_OK;
+}
+
+nvfp4lora_status check_fp8_rows(const void* x, const uint8_t* q, const float* scales, int64_t rows, int64_t H,
+                                int32_t dtype) {
+    if (rows < 1 || H < 1) return fail(NVFP4LORA_ERR_INVALID_ARG, "rows >= 1 and H >= 1 are required (rows=%lld H=%lld)",
+                                       (long long)rows, (long long)H);
+    if (rows > kMaxDim || H > kMaxK) return fail(NVFP4LORA_ERR_INVALID_ARG, "rows <= 2^30 and H <= 2^20 are required");
+    if (!valid_type(dtype)) return fail(NVFP4LORA_ERR_INVALID_ARG, "dtype must be NVFP4LORA_DTYPE_BF16, _FP16 or _FP32");
+    if (!x || !q || !scales) return fail(NVFP4LORA_ERR_INVALID_ARG, "x, q and scales must be non-null");
+    if (!aligned(x, type_bytes(dtype)) || !aligned(scales, 4))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "x must be aligned to its elements and scales 4-byte aligned");
+    return NVFP4LORA_OK;
+}
+
+// ---- the 8-bit product ----
+
+template <OutType OT>
+nvfp4lora_status launch_fp8_pair(DeviceInfo* info, const uint8_t* a, const uint8_t* b, Fp8GemmArgs args, int64_t K,
+                                 cudaStream_t stream) {
+    nvfp4lora_status st;
+    auto kernel = fp8_gemm_pair_kernel<OT>;
+    constexpr int smem = Fp8Smem::DYN_BYTES;
+    if ((st = ensure_smem_attr(info, kernel, smem)) != NVFP4LORA_OK) return st;
+    static std::atomic<int> regs_ok{0};            // one per instantiation
+    if ((st = check_split_regs(kernel, kFp8RegsLaunch, regs_ok, "8-bit product")) != NVFP4LORA_OK) return st;
+    CUtensorMap tm_a, tm_b, tm_out;
+    std::memset(&tm_out, 0, sizeof(tm_out));
+    if ((st = encode_2d(&tm_a, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.M, 128, 128)) != NVFP4LORA_OK) return st;
+    if ((st = encode_2d(&tm_b, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.N, 128, 128)) != NVFP4LORA_OK) return st;
+    constexpr int esize = OT == OutType::FP32 ? 4 : 2;
+    args.vec_out = ((int64_t)args.N * esize) % 16 == 0 && aligned(args.out, 16);
+    if (args.vec_out &&
+        (st = encode_2d(&tm_out, args.out,
+                        OT == OutType::FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                            : OT == OutType::FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        esize, args.N, args.M, kFp8BoxCols, kFp8BoxRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != NVFP4LORA_OK)
+        return st;
+    args.m_tiles = (args.M + kFp8TileM - 1) / kFp8TileM;
+    args.n_tiles = (args.N + kFp8TileN - 1) / kFp8TileN;
+    const int64_t tiles = (int64_t)args.m_tiles * args.n_tiles;
+    if (tiles > INT32_MAX) return fail(NVFP4LORA_ERR_INVALID_ARG, "too many output tiles (M x N too large)");
+    args.num_tiles = (int)tiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, info->sms / 2));
+    cfg.blockDim = dim3(kFp8Threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, tm_out, args);
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit product launch");
+    return NVFP4LORA_OK;
+}
+
+template <int MT, OutType OT>
+nvfp4lora_status launch_fp8_splitk(DeviceInfo* info, const uint8_t* a, const uint8_t* b, const Fp8SplitArgs& args,
+                                   int64_t K, cudaStream_t stream) {
+    nvfp4lora_status st;
+    auto kernel = fp8_splitk_kernel<MT, OT>;
+    constexpr int smem = Fp8SplitPlan<MT>::DYN_BYTES;
+    if ((st = ensure_smem_attr(info, kernel, smem)) != NVFP4LORA_OK) return st;
+    CUtensorMap tm_a, tm_b;
+    if ((st = encode_2d(&tm_a, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.M, 128, MT)) != NVFP4LORA_OK) return st;
+    if ((st = encode_2d(&tm_b, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.N, 128, 128)) != NVFP4LORA_OK) return st;
+    const int64_t m_tiles = (args.M + MT - 1) / MT;
+    if (m_tiles > 65535) return fail(NVFP4LORA_ERR_INVALID_ARG, "too many output tiles (M too large)");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((args.N + 127) / 128), (unsigned)args.splits, (unsigned)m_tiles);
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (args.splits > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = args.splits;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_b, args);
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit product launch (split K)");
+    return NVFP4LORA_OK;
+}
+
+struct Fp8Plan {
+    bool pair;               // the SM-pair kernel
+    int mt, splits;          // the split-K kernel's token tile and cluster size
+};
+
+// The kernel of a shape, by estimated time in units of one K block of a 128 x 128 tile on one SM.
+Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t kblocks, int sms) {
+    Fp8Plan best{false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1};
+    const int64_t tiles = (N + 127) / 128 * ((M + best.mt - 1) / best.mt);
+    double best_cost = 1e30;
+    for (int s = 1; s <= kSplitMaxS && s <= kblocks; ++s) {
+        const int64_t per_sm = (tiles * s + sms - 1) / sms;
+        const double cost = (double)per_sm * ((kblocks + s - 1) / s) + (s > 1 ? 4 : 0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best.splits = s;
+        }
+    }
+    if (M > 128) {
+        const int64_t pairs = (M + kFp8TileM - 1) / kFp8TileM * ((N + kFp8TileN - 1) / kFp8TileN);
+        const double cost = (double)((pairs + sms / 2 - 1) / (sms / 2)) * kblocks * 1.2;
+        best.pair = cost < best_cost;
+    }
+    return best;
+}
+
+template <OutType OT>
+nvfp4lora_status launch_fp8(DeviceInfo* info, const uint8_t* a, const uint8_t* b, const Fp8GemmArgs& g, int64_t K,
+                            cudaStream_t stream) {
+    const Fp8Plan plan = plan_fp8(g.M, g.N, g.kblocks, info->sms);
+    if (plan.pair) return launch_fp8_pair<OT>(info, a, b, g, K, stream);
+    Fp8SplitArgs s;
+    s.a_scale = g.a_scale;
+    s.b_scale = g.b_scale;
+    s.bias = g.bias;
+    s.out = g.out;
+    s.stride_am = g.stride_am;
+    s.stride_ak = g.stride_ak;
+    s.M = g.M;
+    s.N = g.N;
+    s.kblocks = g.kblocks;
+    s.splits = plan.splits;
+    switch (plan.mt) {
+        case 16: return launch_fp8_splitk<16, OT>(info, a, b, s, K, stream);
+        case 32: return launch_fp8_splitk<32, OT>(info, a, b, s, K, stream);
+        case 64: return launch_fp8_splitk<64, OT>(info, a, b, s, K, stream);
+        default: return launch_fp8_splitk<128, OT>(info, a, b, s, K, stream);
+    }
+}
+
 }  // namespace
 }  // namespace nvfp4lora
 
@@ -840,6 +1057,10 @@ nvfp4lora_status nvfp4lora_device_status(nvfp4lora_stream stream) {
                         "LoRA delta: a routing entry was out of range (expert id outside [0, num_experts), "
                         "permuted index past the activation rows, or a null or misaligned bank address); "
                         "that slot was skipped");
+        if (word == kErrBadSlot)
+            return fail(NVFP4LORA_ERR_INVALID_ARG,
+                        "routed tokens: an expert id was not below num_experts, or a permuted index not below the row "
+                        "count; that slot was left out");
         return fail(NVFP4LORA_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait ran out (pipeline stalled)");
     }
     return NVFP4LORA_OK;
@@ -1004,6 +1225,303 @@ nvfp4lora_status nvfp4lora_bgmv_moe_gemm2_lora_delta(
     if (f16_in)
         return f16_out ? pick(bgmv_delta_kernel<true, true>) : pick(bgmv_delta_kernel<true, false>);
     return f16_out ? pick(bgmv_delta_kernel<false, true>) : pick(bgmv_delta_kernel<false, false>);
+}
+
+nvfp4lora_status nvfp4lora_moe_permute(const void* x, int64_t num_tokens, int64_t row_bytes, const int32_t* topk_ids,
+                                       int64_t top_k, int64_t num_experts, int64_t align, int32_t zero_padding,
+                                       void* rows, int64_t padded_rows, int32_t* m_indptr,
+                                       int32_t* expanded_idx_to_permuted_idx, int32_t* permuted_idx_to_expanded_idx,
+                                       void* workspace, int64_t workspace_bytes, nvfp4lora_stream stream) {
+    t_last_error.clear();
+    nvfp4lora_status st = check_routing(num_tokens, top_k, padded_rows);
+    if (st != NVFP4LORA_OK) return st;
+    if (num_experts < 1 || num_experts > kMoeMaxExperts)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "num_experts = %lld: 1 <= num_experts <= %d is required",
+                    (long long)num_experts, kMoeMaxExperts);
+    if (align < 1 || align > kMoeMaxAlign)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "align = %lld: 1 <= align <= %d is required", (long long)align, kMoeMaxAlign);
+    if (row_bytes < 1 || row_bytes > kMaxDim)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "row_bytes = %lld out of range", (long long)row_bytes);
+    const int64_t n = num_tokens * top_k;
+    const int64_t need = (n + std::min(num_experts, n) * (align - 1)) / align * align;
+    if (padded_rows < need)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "padded_rows = %lld: %lld tokens, top_k = %lld, %lld experts and align = %lld "
+                    "can need %lld", (long long)padded_rows, (long long)num_tokens, (long long)top_k,
+                    (long long)num_experts, (long long)align, (long long)need);
+    if (!m_indptr || !aligned(m_indptr, 4))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "m_indptr must be a non-null, 4-byte aligned int32 array");
+    if (n > 0 && (!x || !topk_ids || !rows || !expanded_idx_to_permuted_idx))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "x, topk_ids, rows and the tables must be non-null");
+    if (padded_rows > 0 && !permuted_idx_to_expanded_idx)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "permuted_idx_to_expanded_idx must be non-null");
+    if (!aligned(topk_ids, 4) || !aligned(expanded_idx_to_permuted_idx, 4) || !aligned(permuted_idx_to_expanded_idx, 4))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "topk_ids and the tables must be 4-byte aligned");
+    const bool counted = n > kMoeSelfCountSlots;
+    const int64_t ws = counted ? (int64_t)kMoeCountChunks * num_experts * 4 : 0;
+    if (counted && (!workspace || workspace_bytes < ws || !aligned(workspace, 4)))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "workspace needs %lld bytes, 4-byte aligned (got %lld)", (long long)ws,
+                    (long long)workspace_bytes);
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    PermuteArgs a;
+    a.x = static_cast<const uint8_t*>(x);
+    a.ids = topk_ids;
+    a.rows = static_cast<uint8_t*>(rows);
+    a.indptr = m_indptr;
+    a.idx = expanded_idx_to_permuted_idx;
+    a.inv = permuted_idx_to_expanded_idx;
+    a.counts = nullptr;
+    a.chunk = (n + kMoeCountChunks - 1) / kMoeCountChunks;
+    a.n = n;
+    a.row_bytes = row_bytes;
+    a.T = (int)num_tokens;
+    a.top_k = (int)top_k;
+    a.E = (int)num_experts;
+    a.align = (int)align;
+    a.capacity = (int)padded_rows;
+    a.zero_padding = zero_padding != 0;
+    if (counted) {
+        a.counts = static_cast<int32_t*>(workspace);
+        st = launch_dependent("expert count launch", moe_count_kernel, kMoeCountChunks, kMoeThreads, s, a.ids, a.n, a.chunk,
+                              a.E, static_cast<int32_t*>(workspace));
+        if (st != NVFP4LORA_OK) return st;
+    }
+    // a token per CTA at least, or about eight padding rows; four CTAs per SM at most
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(num_tokens, padded_rows / 8),
+                                                                (int64_t)info->sms * 4));
+    auto go = [&](auto kernel) { return launch_dependent("permute launch", kernel, grid, kMoeThreads, s, a); };
+    auto fits = [&](int64_t v) { return row_bytes % v == 0 && aligned(x, v) && aligned(rows, v); };
+    if (fits(16)) return go(moe_permute_kernel<16>);
+    if (fits(4)) return go(moe_permute_kernel<4>);
+    if (fits(2)) return go(moe_permute_kernel<2>);
+    return go(moe_permute_kernel<1>);
+}
+
+nvfp4lora_status nvfp4lora_moe_unpermute(const void* y, int64_t padded_rows, int64_t H, int32_t dtype,
+                                         const int32_t* expanded_idx_to_permuted_idx, const float* topk_weights,
+                                         int64_t num_tokens, int64_t top_k, void* out, nvfp4lora_stream stream) {
+    t_last_error.clear();
+    nvfp4lora_status st = check_routing(num_tokens, top_k, padded_rows);
+    if (st != NVFP4LORA_OK) return st;
+    if (H < 1 || H > kMaxK) return fail(NVFP4LORA_ERR_INVALID_ARG, "H = %lld: 1 <= H <= 2^20 is required", (long long)H);
+    if (!valid_type(dtype)) return fail(NVFP4LORA_ERR_INVALID_ARG, "dtype must be NVFP4LORA_DTYPE_BF16, _FP16 or _FP32");
+    if (num_tokens == 0) return NVFP4LORA_OK;
+    if (!out || !expanded_idx_to_permuted_idx || (!y && padded_rows > 0))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "y, expanded_idx_to_permuted_idx and out must be non-null");
+    const int es = type_bytes(dtype);
+    if (!aligned(y, es) || !aligned(out, es) || !aligned(expanded_idx_to_permuted_idx, 4) || !aligned(topk_weights, 4))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "y and out must be aligned to their elements, the tables 4-byte aligned");
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
+    const bool vec = rows_aligned16(H * es, {y, out});
+    UnpermuteArgs a;
+    a.y = y;
+    a.idx = expanded_idx_to_permuted_idx;
+    a.w = topk_weights;
+    a.out = out;
+    a.nv = vec ? H * es / 16 : H;
+    a.segs = (int)((a.nv + 31) / 32);
+    a.units = num_tokens * a.segs;
+    a.top_k = (int)top_k;
+    a.rows = (int)padded_rows;
+    const int64_t grid = (a.units + kMoeThreads / 32 - 1) / (kMoeThreads / 32);
+    return by_type(dtype, [&](auto ty) {
+        constexpr MoeType TY = decltype(ty)::value;
+        constexpr int VE = TY == MoeType::FP32 ? 4 : 8;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        return vec ? launch_dependent("unpermute launch", moe_unpermute_kernel<TY, VE>, grid, kMoeThreads, s, a)
+                   : launch_dependent("unpermute launch", moe_unpermute_kernel<TY, 1>, grid, kMoeThreads, s, a);
+    });
+}
+
+nvfp4lora_status nvfp4lora_moe_permute_backward(const void* grad_rows, int64_t padded_rows, int64_t H, int32_t dtype,
+                                                const int32_t* expanded_idx_to_permuted_idx, int64_t num_tokens,
+                                                int64_t top_k, void* grad_x, nvfp4lora_stream stream) {
+    // the sum of a token's rows, each with weight 1
+    return nvfp4lora_moe_unpermute(grad_rows, padded_rows, H, dtype, expanded_idx_to_permuted_idx, nullptr, num_tokens,
+                                   top_k, grad_x, stream);
+}
+
+nvfp4lora_status nvfp4lora_moe_unpermute_backward(const void* grad_out, const void* y, int64_t padded_rows, int64_t H,
+                                                  int32_t dtype, const int32_t* expanded_idx_to_permuted_idx,
+                                                  const int32_t* permuted_idx_to_expanded_idx, const int32_t* m_indptr,
+                                                  int64_t num_experts, const float* topk_weights, int64_t num_tokens,
+                                                  int64_t top_k, void* grad_rows, float* grad_weights,
+                                                  nvfp4lora_stream stream) {
+    t_last_error.clear();
+    nvfp4lora_status st = check_routing(num_tokens, top_k, padded_rows);
+    if (st != NVFP4LORA_OK) return st;
+    if (H < 1 || H > kMaxK) return fail(NVFP4LORA_ERR_INVALID_ARG, "H = %lld: 1 <= H <= 2^20 is required", (long long)H);
+    if (!valid_type(dtype)) return fail(NVFP4LORA_ERR_INVALID_ARG, "dtype must be NVFP4LORA_DTYPE_BF16, _FP16 or _FP32");
+    if (num_experts < 1 || num_experts > kMoeMaxExperts)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "num_experts = %lld: 1 <= num_experts <= %d is required",
+                    (long long)num_experts, kMoeMaxExperts);
+    if ((topk_weights == nullptr) != (grad_weights == nullptr))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "topk_weights and grad_weights go together");
+    if (!m_indptr || !aligned(m_indptr, 4))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "m_indptr must be a non-null, 4-byte aligned int32 array");
+    if (num_tokens == 0 || padded_rows == 0) {
+        if (num_tokens > 0)
+            return fail(NVFP4LORA_ERR_INVALID_ARG, "padded_rows = 0 with num_tokens = %lld", (long long)num_tokens);
+        return NVFP4LORA_OK;
+    }
+    if (!grad_out || !grad_rows || !expanded_idx_to_permuted_idx || !permuted_idx_to_expanded_idx || (topk_weights && !y))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "grad_out, y, grad_rows and the tables must be non-null");
+    const int es = type_bytes(dtype);
+    if (!aligned(grad_out, es) || !aligned(y, es) || !aligned(grad_rows, es) || !aligned(expanded_idx_to_permuted_idx, 4) ||
+        !aligned(permuted_idx_to_expanded_idx, 4) || !aligned(topk_weights, 4) || !aligned(grad_weights, 4))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "rows must be aligned to their elements, the tables 4-byte aligned");
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
+    const bool vec = rows_aligned16(H * es, {grad_out, y, grad_rows});
+    UnpermuteBwdArgs a;
+    a.g = grad_out;
+    a.y = y;
+    a.idx = expanded_idx_to_permuted_idx;
+    a.inv = permuted_idx_to_expanded_idx;
+    a.total = m_indptr + num_experts;
+    a.w = topk_weights;
+    a.gy = grad_rows;
+    a.gw = grad_weights;
+    a.nv = vec ? H * es / 16 : H;
+    a.T = (int)num_tokens;
+    a.top_k = (int)top_k;
+    a.rows = (int)padded_rows;
+    const int block = (int)std::min<int64_t>(kMoeThreads, (a.nv + 31) / 32 * 32);
+    // the padding rows: up to two CTAs per SM
+    const int64_t grid = num_tokens + std::min<int64_t>((padded_rows + 255) / 256, 2 * (int64_t)info->sms);
+    return by_type(dtype, [&](auto ty) {
+        constexpr MoeType TY = decltype(ty)::value;
+        constexpr int VE = TY == MoeType::FP32 ? 4 : 8;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        return vec ? launch_dependent("unpermute gradient launch", moe_unpermute_bwd_kernel<TY, VE>, grid, block, s, a)
+                   : launch_dependent("unpermute gradient launch", moe_unpermute_bwd_kernel<TY, 1>, grid, block, s, a);
+    });
+}
+
+nvfp4lora_status nvfp4lora_fp8_quantize(const void* x, int64_t rows, int64_t H, int32_t dtype, int64_t block_rows,
+                                        uint8_t* q, float* scales, int64_t scale_stride_row, int64_t scale_stride_group,
+                                        nvfp4lora_stream stream) {
+    t_last_error.clear();
+    nvfp4lora_status st = check_fp8_rows(x, q, scales, rows, H, dtype);
+    if (st != NVFP4LORA_OK) return st;
+    if (block_rows != 1 && block_rows != 128)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "block_rows = %lld: 1 or 128 is required", (long long)block_rows);
+    const int64_t groups = (H + 127) / 128, brows = (rows + block_rows - 1) / block_rows;
+    if ((st = check_scale_strides(brows, groups, scale_stride_row, scale_stride_group)) != NVFP4LORA_OK) return st;
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
+    Fp8QuantArgs a = {};
+    a.x = x;
+    a.q = q;
+    a.scales = scales;
+    a.stride_r = scale_stride_row;
+    a.stride_g = scale_stride_group;
+    a.rows = rows;
+    a.H = H;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool vec = H % 8 == 0 && aligned(x, 16) && aligned(q, 8);
+    return by_type(dtype, [&](auto ty) {
+        constexpr MoeType TY = decltype(ty)::value;
+        if (block_rows == 128)
+            return vec ? launch_dependent("quantize launch", quantize_fp8_blocks_kernel<TY>, brows * groups, 256, s, a)
+                       : launch_dependent("quantize launch", blocks_fp8_kernel<TY>, brows * groups, 256, s, a);
+        if (!vec) return launch_dependent("quantize launch", row_fp8_kernel<TY, false>, rows, 256, s, a);
+        const int64_t want = (rows * groups + 15) / 16;
+        return launch_dependent("quantize launch", quantize_fp8_rows_kernel<TY>,
+                                std::min<int64_t>(want, (int64_t)info->sms * 8), 256, s, a);
+    });
+}
+
+nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(const void* x, void* residual, const void* weight, int64_t rows, int64_t H,
+                                                int32_t dtype, float eps, void* norm_out, uint8_t* q, float* scales,
+                                                int64_t scale_stride_row, int64_t scale_stride_group,
+                                                nvfp4lora_stream stream) {
+    t_last_error.clear();
+    nvfp4lora_status st = check_fp8_rows(x, q, scales, rows, H, dtype);
+    if (st != NVFP4LORA_OK) return st;
+    if (!weight) return fail(NVFP4LORA_ERR_INVALID_ARG, "weight must be non-null");
+    if (!(eps >= 0.0f)) return fail(NVFP4LORA_ERR_INVALID_ARG, "eps = %g: a number >= 0 is required", (double)eps);
+    const int es = type_bytes(dtype);
+    if (!aligned(residual, es) || !aligned(weight, es) || !aligned(norm_out, es))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "residual, weight and norm_out must be aligned to their elements");
+    const int64_t groups = (H + 127) / 128;
+    if ((st = check_scale_strides(rows, groups, scale_stride_row, scale_stride_group)) != NVFP4LORA_OK) return st;
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
+    Fp8QuantArgs a = {};
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.norm_out = norm_out;
+    a.q = q;
+    a.scales = scales;
+    a.stride_r = scale_stride_row;
+    a.stride_g = scale_stride_group;
+    a.rows = rows;
+    a.H = H;
+    a.eps = eps;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t nv = H / 8;
+    const bool vec = H % 8 == 0 && nv <= 4 * kNormMaxThreads && aligned(x, 16) && aligned(residual, 16) &&
+                     aligned(weight, 16) && aligned(norm_out, 16) && aligned(q, 8);
+    return by_type(dtype, [&](auto ty) {
+        constexpr MoeType TY = decltype(ty)::value;
+        if (!vec) return launch_dependent("norm launch", row_fp8_kernel<TY, true>, rows, 256, s, a);
+        auto go = [&](auto kernel, int per) {
+            return launch_dependent("norm launch", kernel, rows, (int)(((nv + per - 1) / per + 31) / 32 * 32), s, a);
+        };
+        if (nv <= 256) return go(rmsnorm_fp8_kernel<TY, 1>, 1);
+        if (nv <= 2 * kNormMaxThreads) return go(rmsnorm_fp8_kernel<TY, 2>, 2);
+        return go(rmsnorm_fp8_kernel<TY, 4>, 4);
+    });
+}
+
+nvfp4lora_status nvfp4lora_mm_fp8(const uint8_t* a, const uint8_t* b, const float* a_scale, int64_t a_scale_stride_m,
+                                  int64_t a_scale_stride_k, const float* b_scale, const uint16_t* bias, void* out,
+                                  int32_t out_dtype, int64_t M, int64_t N, int64_t K, nvfp4lora_stream stream) {
+    t_last_error.clear();
+    if (M < 1) return fail(NVFP4LORA_ERR_INVALID_ARG, "M = %lld: M >= 1 is required", (long long)M);
+    if (N < 1) return fail(NVFP4LORA_ERR_INVALID_ARG, "N = %lld: N >= 1 is required", (long long)N);
+    if (K < 16 || K % 16 != 0)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "K = %lld: K must be a positive multiple of 16", (long long)K);
+    if (M > kMaxDim || N > kMaxDim || K > kMaxK)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "M, N <= 2^30 and K <= 2^20 are required");
+    if (!valid_type(out_dtype))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "out_dtype must be NVFP4LORA_DTYPE_BF16, _FP16 or _FP32");
+    if (!a || !b || !a_scale || !b_scale || !out)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "a, b, a_scale, b_scale and out must be non-null");
+    if (!aligned(a, 16) || !aligned(b, 16)) return fail(NVFP4LORA_ERR_INVALID_ARG, "a and b must be 16-byte aligned");
+    if (!aligned(a_scale, 4) || !aligned(b_scale, 4))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "a_scale and b_scale must be 4-byte aligned");
+    if (!aligned(out, type_bytes(out_dtype)) || !aligned(bias, 2))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "out must be aligned to its elements and bias 2-byte aligned");
+    if (a_scale_stride_m < 0 || a_scale_stride_k < 0)
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "a_scale strides must not be negative");
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    nvfp4lora_status st = device_info(&dev, &info);
+    if (st != NVFP4LORA_OK) return st;
+    Fp8GemmArgs g = {};
+    g.a_scale = a_scale;
+    g.b_scale = b_scale;
+    g.bias = bias;
+    g.out = out;
+    g.stride_am = a_scale_stride_m;
+    g.stride_ak = a_scale_stride_k;
+    g.M = (int)M;
+    g.N = (int)N;
+    g.kblocks = (int)((K + 127) / 128);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (out_dtype == NVFP4LORA_DTYPE_BF16) return launch_fp8<OutType::BF16>(info, a, b, g, K, s);
+    if (out_dtype == NVFP4LORA_DTYPE_FP16) return launch_fp8<OutType::FP16>(info, a, b, g, K, s);
+    return launch_fp8<OutType::FP32>(info, a, b, g, K, s);
 }
 
 const char* nvfp4lora_last_error(void) { return t_last_error.c_str(); }

@@ -1,0 +1,354 @@
+// E4M3 x E4M3 product with fp32 scales per block of 128, tiled SM-pair kernel (sm_100a).
+//
+//     out[m, n] = round( sum_kb sa[m, kb] * sb[n / 128, kb] * P_kb[m, n]  [+ bias[n]] ),
+//     P_kb[m, n] = sum over the 128 columns k of block kb of a[m, k] * b[n, k].
+// The scales are general fp32 numbers, so they cannot ride on the tensor cores' own block scaling
+// (powers of two, or e4m3): each P_kb is formed in TMEM by itself, read back and added to an fp32
+// accumulator in registers, acc = fma(sa * sb, P_kb, acc).
+//
+// A cluster of two CTAs computes one 256 x 256 output tile per step with tcgen05.mma.cta_group::2
+// (kind::f8f6f4, M = 256, N = 256, K = 32): each CTA loads its own 128 rows of A and 128 of the
+// tile's 256 B rows, 32 KB per CTA and K block.  The TMEM holds two 256-column accumulators used
+// in turn, so the MMAs of a K block (4 x 128 cycles) run while the eight promotion warps of each
+// CTA read the previous one (128 lanes x 256 columns: one warp per lane quarter and 128 columns,
+// which see a single sb per K block).  Registers are split by warpgroup: the promotion warps hold
+// 128 fp32 sums each.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+
+namespace nvfp4lora {
+
+enum class OutType { BF16 = 0, FP16 = 1, FP32 = 2 };
+
+struct Fp8GemmArgs {
+    const float* a_scale;    // element (m, kb) at m * stride_am + kb * stride_ak
+    const float* b_scale;    // [ceil(N / 128), kblocks] row-major
+    const uint16_t* bias;    // bf16 [N] or null
+    void* out;               // [M, N]
+    int64_t stride_am, stride_ak;
+    int M, N, kblocks;       // kblocks = ceil(K / 128)
+    int m_tiles, n_tiles, num_tiles;
+    int vec_out;             // rows of out 16-byte aligned: TMA stores
+};
+
+// Instruction descriptor: kind::f8f6f4, E4M3 x E4M3 -> fp32, K-major A and B.
+__host__ __device__ constexpr uint32_t idesc_e4m3_m(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// One K = 32 step of a single CTA's MMA (the split-K kernel).
+__device__ __forceinline__ void tc_mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// {a.x, a.y} + s * {p.x, p.y}, each rounded to nearest even (one packed fma)
+__device__ __forceinline__ void fma2(float& ax, float& ay, uint32_t px, uint32_t py, uint64_t ss) {
+    uint64_t d;
+    asm("{\n\t.reg .b64 pa, pp;\n\t"
+        "mov.b64 pa, {%1, %2};\n\t"
+        "mov.b64 pp, {%3, %4};\n\t"
+        "fma.rn.f32x2 %0, pp, %5, pa;\n\t}"
+        : "=l"(d) : "f"(ax), "f"(ay), "r"(px), "r"(py), "l"(ss));
+    ax = __uint_as_float((uint32_t)d);
+    ay = __uint_as_float((uint32_t)(d >> 32));
+}
+
+__device__ __forceinline__ uint64_t dup2(float s) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(s));
+    return d;
+}
+
+// `out` values of one type, packed two (16-bit types) per word.
+template <OutType OT>
+__device__ __forceinline__ uint32_t pack_out2(float a, float b) {
+    if constexpr (OT == OutType::FP16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        uint32_t u;
+        memcpy(&u, &h, 4);
+        return u;
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        uint32_t u;
+        memcpy(&u, &h, 4);
+        return u;
+    }
+}
+
+template <OutType OT>
+__device__ __forceinline__ void store_out_one(void* out, int64_t i, float v) {
+    if constexpr (OT == OutType::FP32) static_cast<float*>(out)[i] = v;
+    else if constexpr (OT == OutType::FP16) static_cast<__half*>(out)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+}
+
+constexpr int kFp8TileM = 256;           // per SM pair: 128 rows per CTA
+constexpr int kFp8TileN = 256;
+constexpr int kFp8Stages = 5;
+constexpr int kFp8Threads = 384;         // warpgroup 0: producer, MMA issuer; 1 and 2: promotion
+constexpr int kFp8EpiWarps = 8;
+constexpr int kFp8BoxCols = 32;
+constexpr int kFp8BoxRows = 32;
+// Registers per thread after the split: the block is launched with 384 x 168 and the shares must not
+// exceed that pool (setmaxnreg.inc waits for registers that the other warpgroup gives back).
+constexpr int kFp8RegsLaunch = 168;
+constexpr int kFp8RegsCtl = 56;
+constexpr int kFp8RegsEpi = 224;
+static_assert(128 * kFp8RegsCtl + 256 * kFp8RegsEpi <= kFp8Threads * kFp8RegsLaunch,
+              "register split exceeds the launch's register pool");
+
+struct Fp8Smem {
+    static constexpr int A_BYTES = 128 * 128;
+    static constexpr int B_BYTES = 128 * 128;
+    static constexpr int STAGE_TX = A_BYTES + B_BYTES;    // per CTA, on the leader's barrier
+    static constexpr int A_OFF = 0;
+    static constexpr int B_OFF = A_OFF + kFp8Stages * A_BYTES;
+    static constexpr int OUT_OFF = B_OFF + kFp8Stages * B_BYTES;
+    static constexpr int BOX_BYTES = kFp8BoxCols * kFp8BoxRows * 4;    // fp32: the widest
+    static constexpr int BAR_OFF = OUT_OFF + kFp8EpiWarps * BOX_BYTES;
+    static constexpr int NUM_BARS = 2 * kFp8Stages + 4 + 1;            // full, empty, acc_full[2], acc_empty[2], drain
+    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
+    static constexpr int TOTAL = MISC_OFF + 16;
+    static constexpr int DYN_BYTES = TOTAL + 1024;
+    static_assert(DYN_BYTES <= 232448, "shared-memory plan exceeds 227 KB");
+};
+
+template <OutType OT>
+__global__ void __launch_bounds__(kFp8Threads, 1)
+fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_out, const Fp8GemmArgs args) {
+    using L = Fp8Smem;
+    constexpr uint32_t IDESC = idesc_e4m3_m(kFp8TileM, kFp8TileN);
+    constexpr uint16_t kBoth = 0x3;
+    constexpr uint32_t kAll = 0xffffffffu;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);   // the leader's is used
+    uint64_t* empty = full + kFp8Stages;
+    uint64_t* acc_full = empty + kFp8Stages;       // [2] a K block's product is complete
+    uint64_t* acc_empty = acc_full + 2;            // [2] the leader's: both CTAs have read it
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();          // 0: the leader, which issues the MMAs
+    const int pair = blockIdx.x >> 1;
+    const int npairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tm_a);
+        prefetch_tensor_map(&tm_b);
+        if (args.vec_out) prefetch_tensor_map(&tm_out);
+        for (int s = 0; s < kFp8Stages; ++s) {
+            mbar_init(&full[s], 1);                // the leader's expect_tx; bytes from both CTAs
+            mbar_init(&empty[s], 1);               // the leader's multicast commit
+        }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&acc_full[k], 1);            // the leader's multicast commit
+            mbar_init(&acc_empty[k], 2 * kFp8EpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // both CTAs' barriers exist before any copy completes on, or any thread arrives at, the peer
+    cluster_arrive();
+    cluster_wait();
+    const uint32_t tmem = *tmem_slot;
+    grid_launch_dependents();
+
+    if (warp < 4) {
+        reg_dealloc<kFp8RegsCtl>();
+        if (warp == 0 && lane == 0) {
+            // ------------------------------- TMA producer (both CTAs) -------------------------------
+            grid_dependency_wait();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
+                const int row_a = (tile % args.m_tiles) * kFp8TileM + (int)rank * 128;   // this CTA's A rows
+                const int row_b = (tile / args.m_tiles) * kFp8TileN + (int)rank * 128;   // and B half
+                for (int kb = 0; kb < args.kblocks; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+                    const uint32_t lead_full = map_to_rank(smem_u32(&full[stage]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE_TX);
+                    tma_load_2d_pair(smem + L::A_OFF + stage * L::A_BYTES, &tm_a, lead_full, kb * 128, row_a);
+                    tma_load_2d_pair(smem + L::B_OFF + stage * L::B_BYTES, &tm_b, lead_full, kb * 128, row_b);
+                    if (++stage == kFp8Stages) { stage = 0; phase ^= 1; }
+                }
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ------------------------------- MMA issuer (the leader) -------------------------------
+            grid_dependency_wait();
+            int stage = 0;
+            uint32_t phase = 0, g = 0;             // g: K blocks issued so far, over all tiles
+            bool ok = true;
+            for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
+                for (int kb = 0; kb < args.kblocks; ++kb, ++g) {
+                    const uint32_t buf = g & 1;
+                    if (!mbar_wait_cluster(&acc_empty[buf], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem + L::A_OFF + stage * L::A_BYTES);
+                    const uint32_t b_addr = smem_u32(smem + L::B_OFF + stage * L::B_BYTES);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        tc_mma_fp8_pair(tmem + buf * kFp8TileN, sdesc_sw128(a_addr + j * 32),
+                                        sdesc_sw128(b_addr + j * 32), IDESC, j > 0 ? 1u : 0u);
+                    tc_commit_pair_multicast(&empty[stage], kBoth);
+                    tc_commit_pair_multicast(&acc_full[buf], kBoth);
+                    if (++stage == kFp8Stages) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (!ok || *abort_flag) {
+                // Wait for the MMAs already issued before TMEM is released.
+                tc_commit_pair_multicast(drain, 0x1);
+                mbar_wait(drain, 0, nullptr);
+            }
+        }
+        __syncwarp();
+    } else {
+        reg_alloc<kFp8RegsEpi>();
+        // ------------------------------- promotion and epilogue (both CTAs) -------------------------------
+        const int ew = warp - 4;                       // 0..7
+        const int q = warp & 3;                        // TMEM lane quarter of this warp
+        const int h = ew >> 2;                         // which 128 of the 256 columns
+        const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+        grid_dependency_wait();
+        const uint32_t lead_acc_empty = map_to_rank(smem_u32(acc_empty), 0);
+        uint32_t g = 0;
+        bool ok = true;
+        for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
+            const int m_blk = tile % args.m_tiles, n_blk = tile / args.m_tiles;
+            const int row0 = m_blk * kFp8TileM + (int)rank * 128 + q * 32;   // this warp's 32 rows
+            const int row = row0 + lane;
+            const int col0 = n_blk * kFp8TileN + h * 128;
+            const float* sa = args.a_scale + (int64_t)min(row, args.M - 1) * args.stride_am;
+            const float* sb = args.b_scale + (int64_t)min(col0 / 128, (args.N - 1) / 128) * args.kblocks;
+            float acc[128];
+#pragma unroll
+            for (int k = 0; k < 128; ++k) acc[k] = 0.0f;
+            float s_next = __ldg(sa) * __ldg(sb);
+            for (int kb = 0; kb < args.kblocks; ++kb, ++g) {
+                const uint32_t buf = g & 1;
+                const uint64_t ss = dup2(s_next);
+                if (kb + 1 < args.kblocks) s_next = __ldg(sa + (kb + 1) * args.stride_ak) * __ldg(sb + kb + 1);
+                if (!__all_sync(kAll, mbar_wait(&acc_full[buf], (g >> 1) & 1, abort_flag))) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t src = tmem + lane_off + buf * kFp8TileN + h * 128;
+                uint32_t p0[32], p1[32];
+                tmem_load_32(src, p0);
+                tmem_load_wait();
+                tmem_load_32(src + 32, p1);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) fma2(acc[k], acc[k + 1], p0[k], p0[k + 1], ss);
+                tmem_load_wait();
+                tmem_load_32(src + 64, p0);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) fma2(acc[32 + k], acc[33 + k], p1[k], p1[k + 1], ss);
+                tmem_load_wait();
+                tmem_load_32(src + 96, p1);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) fma2(acc[64 + k], acc[65 + k], p0[k], p0[k + 1], ss);
+                tmem_load_wait();
+                // this warp holds its share of the product (tcgen05.wait::ld has returned, so the
+                // arrival carries no data: relaxed suffices)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_relaxed(lead_acc_empty + buf * 8);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) fma2(acc[96 + k], acc[97 + k], p1[k], p1[k + 1], ss);
+            }
+            if (!ok) break;
+            if (args.bias != nullptr) {
+#pragma unroll
+                for (int k = 0; k < 128; ++k)
+                    if (col0 + k < args.N)
+                        acc[k] = __fadd_rn(acc[k], __uint_as_float((uint32_t)__ldg(args.bias + col0 + k) << 16));
+            }
+            if (args.vec_out) {
+                constexpr int ROW = OT == OutType::FP32 ? 128 : 64;      // box row bytes
+                uint8_t* box = smem + L::OUT_OFF + ew * L::BOX_BYTES;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (lane == 0) bulk_wait_group_read<0>();            // its previous store has read it
+                    __syncwarp();
+                    uint4* dst = reinterpret_cast<uint4*>(box + lane * ROW);
+                    if constexpr (OT == OutType::FP32) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float* v = acc + c * 32 + k * 4;
+                            dst[k] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                __float_as_uint(v[3]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float* v = acc + c * 32 + k * 8;
+                            dst[k] = make_uint4(pack_out2<OT>(v[0], v[1]), pack_out2<OT>(v[2], v[3]),
+                                                pack_out2<OT>(v[4], v[5]), pack_out2<OT>(v[6], v[7]));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    const int x = col0 + c * kFp8BoxCols;
+                    if (lane == 0 && x < args.N && row0 < args.M) {
+                        tma_store_2d(&tm_out, box, x, row0);
+                        bulk_commit_group();
+                    }
+                }
+            } else if (row < args.M) {
+#pragma unroll
+                for (int k = 0; k < 128; ++k)
+                    if (col0 + k < args.N) store_out_one<OT>(args.out, (int64_t)row * args.N + col0 + k, acc[k]);
+            }
+        }
+        if (args.vec_out && lane == 0) bulk_wait_group_all();
+    }
+
+    // Neither CTA leaves (or gives TMEM back) while the other may still reach its barriers or the
+    // leader's MMAs its TMEM: the whole pair meets here first.
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+}  // namespace nvfp4lora

@@ -1,0 +1,354 @@
+// E4M3 values with an fp32 scale per group of 128: the quantizer and the fused residual addition,
+// root-mean-square norm and quantizer that make the 8-bit product's operands (sm_100a).
+//
+// For a group of values y (1 x 128 along a row, or a block of 128 x 128):
+//     amax = max(max |y|, 2^-100);   scale = amax / 448;   q = E4M3_rne(y * (448 / amax))
+// (448 is E4M3's largest finite value; the bound 2^-100 keeps the scale and its inverse normal
+// numbers, and gives a group of zeros +-0 codes).  The norm's y is
+//     h = x + residual;   residual <- round(h);   y = h * (1 / sqrt(mean(h^2) + eps)) * weight,
+// all in fp32: the sum of squares, y and the group maxima come from the unrounded h, so that q is
+// the only rounding to fewer bits on its path.
+// A NaN stays a NaN in q and is ignored by amax; an infinity makes its group's scale infinite.
+#pragma once
+
+#include <cstdint>
+
+#include "moe.cuh"
+#include "ptx.cuh"
+#include "quantize.cuh"
+
+namespace nvfp4lora {
+
+constexpr int kNormMaxThreads = 512;     // NV = 4 holds a row of 16384 elements
+constexpr float kFp8Max = 448.0f;
+constexpr float kFp8Tiny = 0x1p-100f;
+
+struct Fp8QuantArgs {
+    const void* x;           // [rows, H]
+    void* residual;          // [rows, H] or null (norm only)
+    const void* weight;      // [H] (norm only)
+    void* norm_out;          // [rows, H] or null (norm only)
+    uint8_t* q;              // [rows, H]
+    float* scales;           // element (r, g) at r * stride_r + g * stride_g
+    int64_t stride_r, stride_g;
+    int64_t rows, H;
+    float eps;
+};
+
+// two float32 -> two E4M3 bytes, `a` in the low one (nearest even, saturating; NaN stays NaN)
+__device__ __forceinline__ uint32_t e4m3x2_rn(float a, float b) {
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
+    return two;
+}
+
+__device__ __forceinline__ uint2 e4m3x8_scaled(const float (&y)[8], float inv) {
+    return make_uint2(e4m3x2_rn(y[0] * inv, y[1] * inv) | (e4m3x2_rn(y[2] * inv, y[3] * inv) << 16),
+                      e4m3x2_rn(y[4] * inv, y[5] * inv) | (e4m3x2_rn(y[6] * inv, y[7] * inv) << 16));
+}
+
+__device__ __forceinline__ float abs_max8(const float (&y)[8]) {
+    float m = fmaxf(fabsf(y[0]), fabsf(y[1]));
+#pragma unroll
+    for (int i = 2; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+    return m;
+}
+
+// Eight consecutive elements as fp32 (16-byte loads; 32 bytes of fp32) and back.
+template <MoeType TY>
+struct Row8 {
+    static constexpr int NW = TY == MoeType::FP32 ? 2 : 1;
+    struct Raw { uint4 w[NW]; };
+    static __device__ __forceinline__ Raw load(const void* p, int64_t v) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[v * NW + i];
+        return r;
+    }
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
+        if constexpr (TY == MoeType::FP32) memcpy(f, &r, 32);
+        else MoePack<TY, 8>::unpack(r.w[0], f);
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t v, const float (&f)[8]) {
+        if constexpr (TY == MoeType::FP32) {
+            Raw r;
+            memcpy(&r, f, 32);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(p)[v * 2 + i] = r.w[i];
+        } else {
+            reinterpret_cast<uint4*>(p)[v] = MoePack<TY, 8>::pack(f);
+        }
+    }
+};
+
+template <MoeType TY>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+    float f[1];
+    MoePack<TY, 1>::load(p, i, f);
+    return f[0];
+}
+
+template <MoeType TY>
+__device__ __forceinline__ void store_one(void* p, int64_t i, float y) {
+    const float f[1] = {y};
+    reinterpret_cast<typename MoePack<TY, 1>::V*>(p)[i] = MoePack<TY, 1>::pack(f);
+}
+
+// Sum over the CTA, the same in every thread (fixed order).  `red` holds 32 floats.
+__device__ __forceinline__ float cta_sum(float s, float* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    float t = lane < nw ? red[lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+    return t;
+}
+
+// ---- norm: a CTA per row, the row kept in registers (NV vectors of 8 per thread) ----
+// HBM-bound: 2 + 1 bytes per element (16-bit types), and 4 more with a residual.  H % 8 == 0 and
+// 16-byte aligned rows; a 1 x 128 group is 16 neighbouring lanes.
+template <MoeType TY, int NV>
+__global__ void __launch_bounds__(kNormMaxThreads)
+rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
+    using R = Row8<TY>;
+    __shared__ float red[32];
+    const int nv = (int)(a.H / 8);
+    const int tid = threadIdx.x;
+    const int64_t base = (int64_t)blockIdx.x * nv;
+    float h[NV][8];
+    typename R::Raw wt[NV];
+    // the weight is not written by the kernels before this one on the stream in a program that keeps
+    // it, but it may be: nothing is read before the dependency wait
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float ss = 0.0f;
+    {
+        typename R::Raw xr[NV], rr[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = tid + i * blockDim.x;
+            if (v < nv) {
+                xr[i] = R::load(a.x, base + v);
+                if (a.residual != nullptr) rr[i] = R::load(a.residual, base + v);
+                wt[i] = R::load(a.weight, v);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = tid + i * blockDim.x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+            if (v < nv) {
+                R::unpack(xr[i], h[i]);
+                if (a.residual != nullptr) {
+                    float r[8];
+                    R::unpack(rr[i], r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[i][e] += r[e];
+                    R::store(a.residual, base + v, h[i]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+            }
+        }
+    }
+    const float rms = rsqrtf(cta_sum(ss, red) / (float)a.H + a.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = tid + i * blockDim.x;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+        if (v < nv) {
+            R::unpack(wt[i], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rms * y[e];
+        }
+        float m = abs_max8(y);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        m = fmaxf(m, kFp8Tiny);
+        if (v < nv) {
+            reinterpret_cast<uint2*>(a.q)[base + v] = e4m3x8_scaled(y, __fdiv_rn(kFp8Max, m));
+            if (a.norm_out != nullptr) R::store(a.norm_out, base + v, y);
+            if ((v & 15) == 0) a.scales[blockIdx.x * a.stride_r + (v >> 4) * a.stride_g] = __fdiv_rn(m, kFp8Max);
+        }
+    }
+}
+
+// ---- any row length and alignment: a CTA per row, a warp per group, the row read twice ----
+// NORM = false: the quantizer of x itself.
+template <MoeType TY, bool NORM>
+__global__ void __launch_bounds__(256)
+row_fp8_kernel(const Fp8QuantArgs a) {
+    __shared__ float red[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int64_t base = (int64_t)blockIdx.x * a.H;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    auto load_h = [&](int64_t i) {
+        float h = load_one<TY>(a.x, base + i);
+        if (NORM && a.residual != nullptr) h += load_one<TY>(a.residual, base + i);
+        return h;
+    };
+    float rms = 1.0f;
+    if (NORM) {
+        float ss = 0.0f;
+        for (int64_t i = threadIdx.x; i < a.H; i += blockDim.x) {
+            const float h = load_h(i);
+            ss = fmaf(h, h, ss);
+        }
+        rms = rsqrtf(cta_sum(ss, red) / (float)a.H + a.eps);
+    }
+    const int64_t groups = (a.H + 127) / 128;
+    for (int64_t g = warp; g < groups; g += nw) {
+        float y[4], m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t i = g * 128 + e * 32 + lane;
+            y[e] = 0.0f;
+            if (i < a.H) {
+                y[e] = load_h(i);
+                if (NORM) {
+                    if (a.residual != nullptr) store_one<TY>(a.residual, base + i, y[e]);
+                    y[e] = y[e] * rms * load_one<TY>(a.weight, i);
+                    if (a.norm_out != nullptr) store_one<TY>(a.norm_out, base + i, y[e]);
+                }
+            }
+            m = fmaxf(m, fabsf(y[e]));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        m = fmaxf(m, kFp8Tiny);
+        const float inv = __fdiv_rn(kFp8Max, m);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t i = g * 128 + e * 32 + lane;
+            if (i < a.H) a.q[base + i] = (uint8_t)e4m3x2_rn(y[e] * inv, 0.0f);
+        }
+        if (lane == 0) a.scales[blockIdx.x * a.stride_r + g * a.stride_g] = __fdiv_rn(m, kFp8Max);
+    }
+}
+
+// ---- quantizer, 1 x 128 groups: half a warp per group, four groups' loads in flight per lane ----
+// HBM-bound: 2 bytes read (16-bit types) and 1 written per element.  H % 8 == 0, aligned rows.
+template <MoeType TY>
+__global__ void __launch_bounds__(256)
+quantize_fp8_rows_kernel(const Fp8QuantArgs a) {
+    using R = Row8<TY>;
+    constexpr int UN = TY == MoeType::FP32 ? 2 : 4;
+    const int64_t groups = (a.H + 127) / 128;
+    const int nv = (int)(a.H / 8);
+    const int hl = threadIdx.x & 15;
+    const int64_t total = a.rows * groups;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // half-warp hw of the grid takes the groups hw, hw + step, ...; a warp's lanes stay together
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x / 16);
+    const int64_t first = (int64_t)blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4);
+    for (int64_t g0 = first; g0 - (first & 1) < total; g0 += step * UN) {
+        typename R::Raw raw[UN];
+        int64_t row[UN];
+        int gr[UN];
+        bool on[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int64_t g = g0 + u * step;
+            row[u] = g / groups;
+            gr[u] = (int)(g - row[u] * groups);
+            on[u] = g < total && gr[u] * 16 + hl < nv;
+            if (on[u]) raw[u] = R::load(a.x, row[u] * nv + gr[u] * 16 + hl);
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+            if (on[u]) R::unpack(raw[u], y);
+            float m = abs_max8(y);
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            m = fmaxf(m, kFp8Tiny);
+            if (on[u]) {
+                reinterpret_cast<uint2*>(a.q)[row[u] * nv + gr[u] * 16 + hl] = e4m3x8_scaled(y, __fdiv_rn(kFp8Max, m));
+                if (hl == 0) a.scales[row[u] * a.stride_r + gr[u] * a.stride_g] = __fdiv_rn(m, kFp8Max);
+            }
+        }
+    }
+}
+
+// ---- quantizer, 128 x 128 blocks: a CTA per block, the block kept in registers ----
+template <MoeType TY>
+__global__ void __launch_bounds__(256)
+quantize_fp8_blocks_kernel(const Fp8QuantArgs a) {
+    using R = Row8<TY>;
+    __shared__ float red[8];
+    const int nv = (int)(a.H / 8);
+    const int64_t gcols = (a.H + 127) / 128;
+    const int64_t br = blockIdx.x / gcols, bc = blockIdx.x % gcols;
+    const int c = (int)bc * 16 + (threadIdx.x & 15);
+    const int64_t r0 = br * 128 + (threadIdx.x >> 4);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    typename R::Raw raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c < nv && r0 + i * 16 < a.rows) raw[i] = R::load(a.x, (r0 + i * 16) * nv + c);
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c < nv && r0 + i * 16 < a.rows) {
+            float y[8];
+            R::unpack(raw[i], y);
+            m = fmaxf(m, abs_max8(y));
+        }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = kFp8Tiny;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+    const float inv = __fdiv_rn(kFp8Max, m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c < nv && r0 + i * 16 < a.rows) {
+            float y[8];
+            R::unpack(raw[i], y);
+            reinterpret_cast<uint2*>(a.q)[(r0 + i * 16) * nv + c] = e4m3x8_scaled(y, inv);
+        }
+    if (threadIdx.x == 0) a.scales[br * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);
+}
+
+// ---- 128 x 128 blocks of any row length and alignment: a CTA per block, read twice ----
+template <MoeType TY>
+__global__ void __launch_bounds__(256)
+blocks_fp8_kernel(const Fp8QuantArgs a) {
+    __shared__ float red[8];
+    const int64_t gcols = (a.H + 127) / 128;
+    const int64_t br = blockIdx.x / gcols, bc = blockIdx.x % gcols;
+    const int64_t c = bc * 128 + (threadIdx.x & 127);
+    const int64_t r0 = br * 128 + (threadIdx.x >> 7), r1 = min(a.rows, br * 128 + 128);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float m = 0.0f;
+    if (c < a.H)
+        for (int64_t r = r0; r < r1; r += 2) m = fmaxf(m, fabsf(load_one<TY>(a.x, r * a.H + c)));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = kFp8Tiny;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+    const float inv = __fdiv_rn(kFp8Max, m);
+    if (c < a.H)
+        for (int64_t r = r0; r < r1; r += 2)
+            a.q[r * a.H + c] = (uint8_t)e4m3x2_rn(load_one<TY>(a.x, r * a.H + c) * inv, 0.0f);
+    if (threadIdx.x == 0) a.scales[br * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);
+}
+
+}  // namespace nvfp4lora

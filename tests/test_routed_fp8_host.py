@@ -1,0 +1,166 @@
+"""CPU checks of the routed-token, norm, quantizer and 8-bit product calls: the oracle against torch's
+own conversions and hand-made tables, and every rule that the host refuses before any CUDA call."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import routed_fp8 as R
+
+P, I64, I32, F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from nvfp4_block_scaled_mm_b200.build import build
+    lib = ctypes.CDLL(build(quiet=True))
+    lib.nvfp4lora_last_error.restype = ctypes.c_char_p
+    lib.nvfp4lora_moe_permute.argtypes = [P, I64, I64, P, I64, I64, I64, I32, P, I64, P, P, P, P, I64, P]
+    lib.nvfp4lora_moe_unpermute.argtypes = [P, I64, I64, I32, P, P, I64, I64, P, P]
+    lib.nvfp4lora_moe_permute_backward.argtypes = [P, I64, I64, I32, P, I64, I64, P, P]
+    lib.nvfp4lora_moe_unpermute_backward.argtypes = [P, P, I64, I64, I32, P, P, P, I64, P, I64, I64, P, P, P]
+    lib.nvfp4lora_fp8_quantize.argtypes = [P, I64, I64, I32, I64, P, P, I64, I64, P]
+    lib.nvfp4lora_rmsnorm_fp8_quantize.argtypes = [P, P, P, I64, I64, I32, F32, P, P, P, I64, I64, P]
+    lib.nvfp4lora_mm_fp8.argtypes = [P, P, P, I64, I64, P, P, P, I32, I64, I64, I64, P]
+    return lib
+
+
+def refused(lib, f, ok, bad):
+    args = dict(ok)
+    for k in bad:
+        assert k in args, k
+    args.update(bad)
+    st = f(*args.values(), None)
+    assert st == 1, (bad, st)
+    return lib.nvfp4lora_last_error().decode()
+
+
+PERMUTE = dict(x=0x10000, T=100, row_bytes=64, ids=0x20000, k=4, E=8, align=128, zero=1, rows=0x30000, cap=1408,
+               indptr=0x40000, idx=0x50000, inv=0x60000, ws=None, ws_bytes=0)
+
+
+@pytest.mark.parametrize("bad,word", [
+    (dict(T=-1), "num_tokens"), (dict(k=0), "top_k"), (dict(k=17), "top_k"), (dict(E=0), "num_experts"),
+    (dict(E=1025), "num_experts"), (dict(align=0), "align"), (dict(align=4097), "align"), (dict(row_bytes=0), "row_bytes"),
+    (dict(cap=1279), "padded_rows"), (dict(indptr=None), "m_indptr"), (dict(indptr=0x40002), "m_indptr"),
+    (dict(x=None), "non-null"), (dict(ids=None), "non-null"), (dict(rows=None), "non-null"), (dict(idx=None), "non-null"),
+    (dict(inv=None), "non-null"), (dict(ids=0x20001), "4-byte aligned"),
+    (dict(T=5000, cap=1 << 20), "workspace"), (dict(T=5000, cap=1 << 20, ws=0x70000, ws_bytes=64 * 8 * 4 - 1), "workspace"),
+    (dict(T=1 << 29), "too large"), (dict(cap=1 << 31), "padded_rows"),
+])
+def test_permute_rules(lib, bad, word):
+    assert word in refused(lib, lib.nvfp4lora_moe_permute, PERMUTE, bad)
+
+
+UNPERMUTE = dict(y=0x10000, rows=512, H=64, dtype=0, idx=0x20000, w=0x30000, T=100, k=4, out=0x40000)
+
+
+@pytest.mark.parametrize("bad,word", [
+    (dict(T=-1), "num_tokens"), (dict(k=0), "top_k"), (dict(k=17), "top_k"), (dict(H=0), "H = 0"), (dict(dtype=3), "dtype"),
+    (dict(dtype=-1), "dtype"), (dict(y=None), "non-null"), (dict(idx=None), "non-null"), (dict(out=None), "non-null"),
+    (dict(y=0x10001), "aligned"), (dict(dtype=2, out=0x40002), "aligned"), (dict(w=0x30002), "aligned"), (dict(rows=-1), "padded_rows"),
+])
+def test_unpermute_rules(lib, bad, word):
+    assert word in refused(lib, lib.nvfp4lora_moe_unpermute, UNPERMUTE, bad)
+    if "w" not in bad:
+        ok = {k: v for k, v in UNPERMUTE.items() if k != "w"}
+        assert word in refused(lib, lib.nvfp4lora_moe_permute_backward, ok, bad)
+
+
+BACKWARD = dict(g=0x10000, y=0x18000, rows=512, H=64, dtype=0, idx=0x20000, inv=0x28000, indptr=0x30000, E=4, w=0x38000,
+                T=100, k=4, gy=0x40000, gw=0x48000)
+
+
+@pytest.mark.parametrize("bad,word", [
+    (dict(k=17), "top_k"), (dict(H=0), "H = 0"), (dict(dtype=7), "dtype"), (dict(E=0), "num_experts"), (dict(gw=None), "go together"),
+    (dict(w=None), "go together"), (dict(indptr=None), "m_indptr"), (dict(g=None), "non-null"), (dict(y=None), "non-null"),
+    (dict(inv=None), "non-null"), (dict(gy=None), "non-null"), (dict(gy=0x40001), "aligned"), (dict(rows=0), "padded_rows"),
+])
+def test_unpermute_backward_rules(lib, bad, word):
+    assert word in refused(lib, lib.nvfp4lora_moe_unpermute_backward, BACKWARD, bad)
+
+
+QUANT = dict(x=0x10000, rows=10, H=300, dtype=0, block_rows=1, q=0x20000, scales=0x30000, sr=1, sg=10)
+
+
+@pytest.mark.parametrize("bad,word", [
+    (dict(rows=0), "rows >= 1"), (dict(H=0), "H >= 1"), (dict(H=1 << 21), "2^20"), (dict(dtype=5), "dtype"),
+    (dict(block_rows=64), "block_rows"), (dict(x=None), "non-null"), (dict(q=None), "non-null"), (dict(scales=None), "non-null"),
+    (dict(scales=0x30002), "aligned"), (dict(dtype=2, x=0x10002), "aligned"), (dict(sg=9), "overlap"), (dict(sr=0, sg=0), "overlap"),
+    (dict(sr=-1), "overlap"), (dict(sr=2, sg=1), "overlap"),
+])
+def test_quantize_rules(lib, bad, word):
+    assert word in refused(lib, lib.nvfp4lora_fp8_quantize, QUANT, bad)
+
+
+NORM = dict(x=0x10000, res=0x18000, weight=0x20000, rows=10, H=300, dtype=0, eps=1e-6, norm=None, q=0x28000, scales=0x30000,
+            sr=3, sg=1)
+
+
+@pytest.mark.parametrize("bad,word", [
+    (dict(weight=None), "weight"), (dict(eps=-1.0), "eps"), (dict(eps=float("nan")), "eps"), (dict(res=0x18001), "aligned"),
+    (dict(norm=0x19001), "aligned"), (dict(rows=0), "rows >= 1"), (dict(sr=2), "overlap"),
+])
+def test_norm_rules(lib, bad, word):
+    assert word in refused(lib, lib.nvfp4lora_rmsnorm_fp8_quantize, NORM, bad)
+
+
+MM = dict(a=0x10000, b=0x20000, sa=0x30000, sm=1, sk=16, sb=0x40000, bias=None, out=0x50000, dtype=0, M=16, N=256, K=256)
+
+
+@pytest.mark.parametrize("bad,word", [
+    (dict(M=0), "M >= 1"), (dict(N=0), "N >= 1"), (dict(K=0), "multiple of 16"), (dict(K=24), "multiple of 16"),
+    (dict(M=1 << 31), "2^30"), (dict(K=1 << 21), "2^20"), (dict(dtype=3), "out_dtype"), (dict(a=None), "non-null"),
+    (dict(sb=None), "non-null"), (dict(out=None), "non-null"), (dict(a=0x10008), "16-byte aligned"), (dict(b=0x20001), "16-byte aligned"),
+    (dict(sa=0x30002), "4-byte aligned"), (dict(out=0x50001), "aligned"), (dict(bias=0x60001), "aligned"), (dict(sk=-1), "negative"),
+])
+def test_mm_rules(lib, bad, word):
+    assert word in refused(lib, lib.nvfp4lora_mm_fp8, MM, bad)
+
+
+def test_binding_refuses_tensors_of_the_host():
+    import nvfp4_block_scaled_mm_b200 as L
+    x, ids = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32)
+    f8 = torch.zeros(4, 128, dtype=torch.float8_e4m3fn)
+    s = torch.ones(4, 1)
+    for call in (lambda: L.moe_permute(x, ids, 4), lambda: L.moe_unpermute(x, ids), lambda: L.moe_permute_backward(x, ids),
+                 lambda: L.moe_unpermute_backward(x, x, ids, ids, ids), lambda: L.fp8_quantize(x),
+                 lambda: L.add_rmsnorm_fp8_quantize(x, x[0]), lambda: L.mm_fp8(f8, f8, s, s)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
+def test_capacity_holds_the_worst_routing():
+    import nvfp4_block_scaled_mm_b200 as L
+    for T, k, E, align in ((1, 1, 1, 128), (5, 2, 4, 128), (64, 2, 8, 128), (7, 3, 5, 8), (0, 2, 4, 128), (3, 16, 2, 1)):
+        cap = L.moe_capacity(T, k, E, align)
+        assert cap == R.moe_capacity(T, k, E, align)
+        n = T * k
+        # as many experts as possible with one row past a multiple of the alignment
+        ids = np.minimum(np.arange(n), E - 1).reshape(T, k) if n else np.zeros((0, k), dtype=np.int64)
+        assert R.moe_tables(ids, E, align, cap)[0][-1] <= cap
+
+
+def test_oracle_tables_by_hand():
+    ids = np.array([[1, 0], [-1, 1], [1, 1]])
+    indptr, idx, inv = R.moe_tables(ids, 3, 2, 8)
+    assert indptr.tolist() == [0, 2, 6, 6]
+    assert idx.tolist() == [[2, 0], [-1, 3], [4, 5]]
+    assert inv.tolist() == [1, -1, 0, 3, 4, 5, -1, -1]
+
+
+def test_oracle_e4m3_is_torch_s():
+    v = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(np.isnan(v), np.isnan(R.E4M3)) and np.array_equal(v[~np.isnan(v)], R.E4M3[~np.isnan(v)])
+    x = torch.cat([torch.randn(20000) * s for s in (1e-3, 1.0, 100.0)]).clamp(-448, 448)
+    x = torch.cat([x, torch.tensor([0.0, -0.0, 2.0 ** -10, 3 * 2.0 ** -10, 17.0, 19.0, 448.0, -448.0])])
+    assert np.array_equal(R.e4m3_encode(x.numpy()), x.to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+def test_oracle_norm_gradient_free_identities():
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((3, 40))
+    h, y = R.add_rmsnorm(x, x, np.ones(40), 0.0)
+    assert np.allclose(h, 2 * x) and np.allclose((y * y).mean(axis=1), 1.0)
