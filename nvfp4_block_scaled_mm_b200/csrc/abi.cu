@@ -766,12 +766,13 @@ nvfp4lora_status launch_fp8_pair(DeviceInfo* info, const uint8_t* a, const uint8
                         OT == OutType::FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                             : OT == OutType::FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        esize, args.N, args.M, kFp8BoxCols, kFp8BoxRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != NVFP4LORA_OK)
+                        esize, args.N, args.M, 64 / esize, kFp8BoxRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != NVFP4LORA_OK)
         return st;
     args.m_tiles = (args.M + kFp8TileM - 1) / kFp8TileM;
     args.n_tiles = (args.N + kFp8TileN - 1) / kFp8TileN;
     const int64_t tiles = (int64_t)args.m_tiles * args.n_tiles;
-    if (tiles > INT32_MAX) return fail(NVFP4LORA_ERR_INVALID_ARG, "too many output tiles (M x N too large)");
+    if (tiles > INT32_MAX - info->sms)       // a tile index one wave past the last stays in int32
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "too many output tiles (M x N too large)");
     args.num_tiles = (int)tiles;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, info->sms / 2));
@@ -806,7 +807,7 @@ nvfp4lora_status launch_fp8_splitk(DeviceInfo* info, const uint8_t* a, const uin
     if (m_tiles > 65535) return fail(NVFP4LORA_ERR_INVALID_ARG, "too many output tiles (M too large)");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((args.N + 127) / 128), (unsigned)args.splits, (unsigned)m_tiles);
-    cfg.blockDim = dim3(kSplitThreads);
+    cfg.blockDim = dim3(Fp8SplitPlan<MT>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -868,6 +869,8 @@ nvfp4lora_status launch_fp8(DeviceInfo* info, const uint8_t* a, const uint8_t* b
     s.N = g.N;
     s.kblocks = g.kblocks;
     s.splits = plan.splits;
+    constexpr int esize = OT == OutType::FP32 ? 4 : 2;
+    s.vec_out = g.N % 4 == 0 && aligned(g.out, 4 * esize);
     switch (plan.mt) {
         case 16: return launch_fp8_splitk<16, OT>(info, a, b, s, K, stream);
         case 32: return launch_fp8_splitk<32, OT>(info, a, b, s, K, stream);

@@ -19,6 +19,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "ptx.cuh"
 
@@ -61,6 +62,46 @@ __device__ __forceinline__ void tc_mma_fp8(uint32_t d_tmem, uint64_t a_desc, uin
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// True in one lane of a converged warp.  A warp that issues MMAs runs its loop with all lanes and issues
+// under this predicate: the compiler then keeps the descriptors in uniform registers.  Issued by
+// `lane == 0` code each MMA waited for its operands to be moved there (about 70 cycles).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait whose try_wait carries no suspend-time hint: the hand-off of a K block's product passes
+// through three of these, and with the 1 ms hint of mbar_wait each woke later (8192 x 28672 x 8192: 1556 us
+// against 1504).  Polling with test_wait instead took issue slots from the promotion warps (1654 us).
+__device__ __forceinline__ bool mbar_try_wait_short(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait_short(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait_short(bar, parity)) return true;
+        if (abort != nullptr && *abort) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            if (abort != nullptr) *abort = 1;
+            atomicExch(&g_device_error, kErrTimeout);
+            return false;
+        }
+    }
 }
 
 // {a.x, a.y} + s * {p.x, p.y}, each rounded to nearest even (one packed fma)
@@ -106,16 +147,15 @@ __device__ __forceinline__ void store_out_one(void* out, int64_t i, float v) {
 
 constexpr int kFp8TileM = 256;           // per SM pair: 128 rows per CTA
 constexpr int kFp8TileN = 256;
-constexpr int kFp8Stages = 5;
+constexpr int kFp8Stages = 6;
 constexpr int kFp8Threads = 384;         // warpgroup 0: producer, MMA issuer; 1 and 2: promotion
 constexpr int kFp8EpiWarps = 8;
-constexpr int kFp8BoxCols = 32;
 constexpr int kFp8BoxRows = 32;
 // Registers per thread after the split: the block is launched with 384 x 168 and the shares must not
 // exceed that pool (setmaxnreg.inc waits for registers that the other warpgroup gives back).
 constexpr int kFp8RegsLaunch = 168;
-constexpr int kFp8RegsCtl = 56;
-constexpr int kFp8RegsEpi = 224;
+constexpr int kFp8RegsCtl = 72;
+constexpr int kFp8RegsEpi = 216;
 static_assert(128 * kFp8RegsCtl + 256 * kFp8RegsEpi <= kFp8Threads * kFp8RegsLaunch,
               "register split exceeds the launch's register pool");
 
@@ -126,7 +166,7 @@ struct Fp8Smem {
     static constexpr int A_OFF = 0;
     static constexpr int B_OFF = A_OFF + kFp8Stages * A_BYTES;
     static constexpr int OUT_OFF = B_OFF + kFp8Stages * B_BYTES;
-    static constexpr int BOX_BYTES = kFp8BoxCols * kFp8BoxRows * 4;    // fp32: the widest
+    static constexpr int BOX_BYTES = 64 * kFp8BoxRows;    // 32 columns of a 16-bit type, 16 of fp32
     static constexpr int BAR_OFF = OUT_OFF + kFp8EpiWarps * BOX_BYTES;
     static constexpr int NUM_BARS = 2 * kFp8Stages + 4 + 1;            // full, empty, acc_full[2], acc_empty[2], drain
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
@@ -134,6 +174,18 @@ struct Fp8Smem {
     static constexpr int DYN_BYTES = TOTAL + 1024;
     static_assert(DYN_BYTES <= 232448, "shared-memory plan exceeds 227 KB");
 };
+
+// Tile order: bands of kFp8Band m tiles, m fastest within a band, so that the pairs running at one time
+// share both operands' tiles.
+constexpr int kFp8Band = 8;
+
+__device__ __forceinline__ void fp8_tile(int tile, int m_tiles, int n_tiles, int& m_blk, int& n_blk) {
+    const int band = tile / (kFp8Band * n_tiles);
+    const int r = tile - band * kFp8Band * n_tiles;
+    const int bm = min(kFp8Band, m_tiles - band * kFp8Band);
+    n_blk = r / bm;
+    m_blk = band * kFp8Band + r - n_blk * bm;
+}
 
 template <OutType OT>
 __global__ void __launch_bounds__(kFp8Threads, 1)
@@ -199,8 +251,10 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
             uint32_t phase = 0;
             bool ok = true;
             for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
-                const int row_a = (tile % args.m_tiles) * kFp8TileM + (int)rank * 128;   // this CTA's A rows
-                const int row_b = (tile / args.m_tiles) * kFp8TileN + (int)rank * 128;   // and B half
+                int m_blk, n_blk;
+                fp8_tile(tile, args.m_tiles, args.n_tiles, m_blk, n_blk);
+                const int row_a = m_blk * kFp8TileM + (int)rank * 128;   // this CTA's A rows
+                const int row_b = n_blk * kFp8TileN + (int)rank * 128;   // and B half
                 for (int kb = 0; kb < args.kblocks; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
                     const uint32_t lead_full = map_to_rank(smem_u32(&full[stage]), 0);
@@ -210,7 +264,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                     if (++stage == kFp8Stages) { stage = 0; phase ^= 1; }
                 }
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // ------------------------------- MMA issuer (the leader) -------------------------------
             grid_dependency_wait();
             int stage = 0;
@@ -219,24 +273,30 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
             for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
                 for (int kb = 0; kb < args.kblocks; ++kb, ++g) {
                     const uint32_t buf = g & 1;
-                    if (!mbar_wait_cluster(&acc_empty[buf], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
-                    if (!mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+                    ok = mbar_wait_short(&full[stage], phase, abort_flag) &&
+                         mbar_wait_short(&acc_empty[buf], ((g >> 1) & 1) ^ 1, abort_flag);
+                    if (!__all_sync(kAll, ok)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(smem + L::A_OFF + stage * L::A_BYTES);
                     const uint32_t b_addr = smem_u32(smem + L::B_OFF + stage * L::B_BYTES);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        tc_mma_fp8_pair(tmem + buf * kFp8TileN, sdesc_sw128(a_addr + j * 32),
-                                        sdesc_sw128(b_addr + j * 32), IDESC, j > 0 ? 1u : 0u);
-                    tc_commit_pair_multicast(&empty[stage], kBoth);
-                    tc_commit_pair_multicast(&acc_full[buf], kBoth);
+                        for (int j = 0; j < 4; ++j)
+                            tc_mma_fp8_pair(tmem + buf * kFp8TileN, sdesc_sw128(a_addr + j * 32),
+                                            sdesc_sw128(b_addr + j * 32), IDESC, j > 0 ? 1u : 0u);
+                        tc_commit_pair_multicast(&acc_full[buf], kBoth);
+                        tc_commit_pair_multicast(&empty[stage], kBoth);
+                    }
+                    __syncwarp();
                     if (++stage == kFp8Stages) { stage = 0; phase ^= 1; }
                 }
             }
             if (!ok || *abort_flag) {
                 // Wait for the MMAs already issued before TMEM is released.
-                tc_commit_pair_multicast(drain, 0x1);
-                mbar_wait(drain, 0, nullptr);
+                if (elect_one()) {
+                    tc_commit_pair_multicast(drain, 0x1);
+                    mbar_wait(drain, 0, nullptr);
+                }
             }
         }
         __syncwarp();
@@ -252,88 +312,86 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
         uint32_t g = 0;
         bool ok = true;
         for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
-            const int m_blk = tile % args.m_tiles, n_blk = tile / args.m_tiles;
+            int m_blk, n_blk;
+            fp8_tile(tile, args.m_tiles, args.n_tiles, m_blk, n_blk);
             const int row0 = m_blk * kFp8TileM + (int)rank * 128 + q * 32;   // this warp's 32 rows
-            const int row = row0 + lane;
             const int col0 = n_blk * kFp8TileN + h * 128;
-            const float* sa = args.a_scale + (int64_t)min(row, args.M - 1) * args.stride_am;
+            const float* sa = args.a_scale + (int64_t)min(row0 + lane, args.M - 1) * args.stride_am;
             const float* sb = args.b_scale + (int64_t)min(col0 / 128, (args.N - 1) / 128) * args.kblocks;
             float acc[128];
 #pragma unroll
             for (int k = 0; k < 128; ++k) acc[k] = 0.0f;
-            float s_next = __ldg(sa) * __ldg(sb);
+            // the scales of the next block, loaded one block ahead; they are multiplied when used (a multiply
+            // here would stall the warp on the loads)
+            float sa_next = __ldg(sa), sb_next = __ldg(sb);
             for (int kb = 0; kb < args.kblocks; ++kb, ++g) {
                 const uint32_t buf = g & 1;
-                const uint64_t ss = dup2(s_next);
-                if (kb + 1 < args.kblocks) s_next = __ldg(sa + (kb + 1) * args.stride_ak) * __ldg(sb + kb + 1);
-                if (!__all_sync(kAll, mbar_wait(&acc_full[buf], (g >> 1) & 1, abort_flag))) { ok = false; break; }
+                const uint64_t ss = dup2(sa_next * sb_next);
+                if (kb + 1 < args.kblocks) {
+                    sa_next = __ldg(sa + (kb + 1) * args.stride_ak);
+                    sb_next = __ldg(sb + kb + 1);
+                }
+                if (!__all_sync(kAll, mbar_wait_short(&acc_full[buf], (g >> 1) & 1, abort_flag))) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t src = tmem + lane_off + buf * kFp8TileN + h * 128;
-                uint32_t p0[32], p1[32];
-                tmem_load_32(src, p0);
-                tmem_load_wait();
-                tmem_load_32(src + 32, p1);
+                uint32_t p[2][16];
+                tmem_load_16(src, p[0]);
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) fma2(acc[k], acc[k + 1], p0[k], p0[k + 1], ss);
-                tmem_load_wait();
-                tmem_load_32(src + 64, p0);
+                for (int c = 0; c < 8; ++c) {
+                    tmem_load_wait();
+                    if (c < 7) tmem_load_16(src + 16 * (c + 1), p[(c + 1) & 1]);
+                    else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote_relaxed(lead_acc_empty + buf * 8);
+                    }
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) fma2(acc[32 + k], acc[33 + k], p1[k], p1[k + 1], ss);
-                tmem_load_wait();
-                tmem_load_32(src + 96, p1);
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) fma2(acc[64 + k], acc[65 + k], p0[k], p0[k + 1], ss);
-                tmem_load_wait();
-                // this warp holds its share of the product (tcgen05.wait::ld has returned, so the
-                // arrival carries no data: relaxed suffices)
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote_relaxed(lead_acc_empty + buf * 8);
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) fma2(acc[96 + k], acc[97 + k], p1[k], p1[k + 1], ss);
+                    for (int k = 0; k < 16; k += 2) fma2(acc[c * 16 + k], acc[c * 16 + k + 1], p[c & 1][k], p[c & 1][k + 1], ss);
+                }
             }
             if (!ok) break;
-            if (args.bias != nullptr) {
+            // 64 bytes of each of the warp's 32 rows at a time through its box in shared memory
+            using E = typename std::conditional<OT == OutType::FP32, uint32_t, uint16_t>::type;
+            constexpr int COLS = 64 / (int)sizeof(E);
+            uint8_t* box = smem + L::OUT_OFF + ew * L::BOX_BYTES;
 #pragma unroll
-                for (int k = 0; k < 128; ++k)
-                    if (col0 + k < args.N)
-                        acc[k] = __fadd_rn(acc[k], __uint_as_float((uint32_t)__ldg(args.bias + col0 + k) << 16));
-            }
-            if (args.vec_out) {
-                constexpr int ROW = OT == OutType::FP32 ? 128 : 64;      // box row bytes
-                uint8_t* box = smem + L::OUT_OFF + ew * L::BOX_BYTES;
+            for (int x = 0; x < 128; x += COLS) {
+                if (col0 + x >= args.N) break;
+                if (args.bias != nullptr) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (lane == 0) bulk_wait_group_read<0>();            // its previous store has read it
-                    __syncwarp();
-                    uint4* dst = reinterpret_cast<uint4*>(box + lane * ROW);
-                    if constexpr (OT == OutType::FP32) {
+                    for (int k = 0; k < COLS; ++k)
+                        acc[x + k] = __fadd_rn(acc[x + k], __uint_as_float((uint32_t)__ldg(args.bias + min(col0 + x + k, args.N - 1)) << 16));
+                }
+                if (args.vec_out && lane == 0) bulk_wait_group_read<0>();   // its previous store has read the box
+                __syncwarp();
+                uint4* dst = reinterpret_cast<uint4*>(box + lane * 64);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float* v = acc + c * 32 + k * 4;
-                            dst[k] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                __float_as_uint(v[3]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float* v = acc + c * 32 + k * 8;
-                            dst[k] = make_uint4(pack_out2<OT>(v[0], v[1]), pack_out2<OT>(v[2], v[3]),
-                                                pack_out2<OT>(v[4], v[5]), pack_out2<OT>(v[6], v[7]));
-                        }
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const float* v = acc + x + k * (COLS / 4);
+                    if constexpr (OT == OutType::FP32)
+                        dst[k] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                            __float_as_uint(v[3]));
+                    else
+                        dst[k] = make_uint4(pack_out2<OT>(v[0], v[1]), pack_out2<OT>(v[2], v[3]),
+                                            pack_out2<OT>(v[4], v[5]), pack_out2<OT>(v[6], v[7]));
+                }
+                if (args.vec_out) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    const int x = col0 + c * kFp8BoxCols;
-                    if (lane == 0 && x < args.N && row0 < args.M) {
-                        tma_store_2d(&tm_out, box, x, row0);
+                    if (lane == 0 && row0 < args.M) {
+                        tma_store_2d(&tm_out, box, col0 + x, row0);
                         bulk_commit_group();
                     }
+                } else {
+                    // rows of out off their 16-byte boundaries: neighbouring lanes store neighbouring columns
+                    __syncwarp();
+                    const int cx = lane % COLS, n = col0 + x + cx;
+                    if (n < args.N)
+                        for (int r = lane / COLS; r < 32 && row0 + r < args.M; r += 32 / COLS)
+                            static_cast<E*>(args.out)[(int64_t)(row0 + r) * args.N + n] =
+                                reinterpret_cast<const E*>(box)[r * COLS + cx];
+                    __syncwarp();
                 }
-            } else if (row < args.M) {
-#pragma unroll
-                for (int k = 0; k < 128; ++k)
-                    if (col0 + k < args.N) store_out_one<OT>(args.out, (int64_t)row * args.N + col0 + k, acc[k]);
             }
         }
         if (args.vec_out && lane == 0) bulk_wait_group_all();

@@ -6,12 +6,12 @@
 //   * CTA r of a cluster takes the K blocks [kb r / S, kb (r + 1) / S) of one 128 x MT tile: a TMA
 //     ring of 128 x 128 weight tiles and MT x 128 token tiles, one MMA thread (kind::f8f6f4, M = 128,
 //     N = MT, four K = 32 steps per block), each block's product into the next of NB accumulators;
-//   * four warps read each product back and add it to fp32 sums, acc[m] += (sa[m, kb] sb[kb]) * P[m];
+//   * promotion warps read each product back and add it to fp32 sums, acc[m] += (sa[m, kb] sb[kb]) * P[m];
 //     a lane is a weight row, so the CTA's products of scales, one per token and block, are staged in
 //     shared memory eight blocks at a time and read as broadcasts;
-//   * the S partial sums meet in distributed shared memory: CTA r receives every CTA's share of the
-//     token columns [MT r / S, MT (r + 1) / S), adds them in rank order and rounds once, so the result
-//     does not depend on the schedule.
+//   * the S partial sums meet in distributed shared memory: CTA r reads every CTA's sums of the token
+//     columns [MT r / S, MT (r + 1) / S), adds them in rank order and rounds once, so the result does
+//     not depend on the schedule.
 // At a decode step the kernel is bound by streaming the weights from HBM.
 #pragma once
 
@@ -23,7 +23,6 @@
 
 namespace nvfp4lora {
 
-constexpr int kSplitThreads = 192;       // warp 0: producer, 1: MMA issuer, 2..5: promotion
 constexpr int kSplitMaxS = 8;
 constexpr int kSplitScaleChunk = 8;      // K blocks whose scale products are staged at a time
 
@@ -34,6 +33,7 @@ struct Fp8SplitArgs {
     void* out;               // [M, N]
     int64_t stride_am, stride_ak;
     int M, N, kblocks, splits;
+    int vec_out;             // rows of out aligned to four elements
 };
 
 template <int MT>
@@ -42,6 +42,10 @@ struct Fp8SplitPlan {
     static constexpr int X_BYTES = MT * 128;
     // MT <= 64: two CTAs per SM (shared memory, registers and TMEM allow both)
     static constexpr int STAGES = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 4 : 6;
+    // promotion warps: one per TMEM lane quarter, and two for 128 columns (64 sums per thread)
+    static constexpr int EW = MT == 128 ? 8 : 4;
+    static constexpr int THREADS = 64 + 32 * EW;                      // warp 0: producer, 1: MMA issuer
+    static constexpr int COLS = MT * 4 / EW;                          // token columns per promotion thread
     static constexpr int NB = MT <= 32 ? 8 : MT == 64 ? 4 : 2;        // accumulators
     static constexpr int TMEM_COLS = NB * MT;                         // 128 or 256: a power of two
     static constexpr int W_OFF = 0;
@@ -52,20 +56,36 @@ struct Fp8SplitPlan {
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int TOTAL = MISC_OFF + 16;
     static constexpr int DYN_BYTES = TOTAL + 1024;
-    // the partial sums of the exchange take the ring's place: S x ceil(MT / S) x 128 floats
-    static_assert((MT + kSplitMaxS) * 128 * 4 <= STAGES * (W_BYTES + X_BYTES), "partials exceed the ring");
+    // the finished sums take the ring's place: [MT][128] floats
+    static_assert(MT * 128 * 4 <= STAGES * (W_BYTES + X_BYTES), "partials exceed the ring");
     static_assert(X_BYTES % 1024 == 0, "token tiles must stay 1024-byte aligned");
     static_assert(DYN_BYTES <= (MT <= 64 ? 113 * 1024 : 227 * 1024), "split-K shared-memory plan too large");
 };
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t caddr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(caddr), "f"(v) : "memory");
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t caddr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(caddr) : "memory");
+    return v;
 }
 
-constexpr uint32_t kSplitScaleBarrier = 1;       // named barrier: the four promotion warps
+// {a.x, a.y} + {s.x, s.y} * {p.x, p.y}, each rounded to nearest even (one packed fma)
+__device__ __forceinline__ void fma2_pair(float& ax, float& ay, uint32_t px, uint32_t py, float sx, float sy) {
+    uint64_t d;
+    asm("{\n\t.reg .b64 pa, pp, ps;\n\t"
+        "mov.b64 pa, {%1, %2};\n\t"
+        "mov.b64 pp, {%3, %4};\n\t"
+        "mov.b64 ps, {%5, %6};\n\t"
+        "fma.rn.f32x2 %0, pp, ps, pa;\n\t}"
+        : "=l"(d) : "f"(ax), "f"(ay), "r"(px), "r"(py), "f"(sx), "f"(sy));
+    ax = __uint_as_float((uint32_t)d);
+    ay = __uint_as_float((uint32_t)(d >> 32));
+}
+
+constexpr uint32_t kSplitScaleBarrier = 1;       // named barrier: the promotion warps
 
 template <int MT, OutType OT>
-__global__ void __launch_bounds__(kSplitThreads, MT <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(Fp8SplitPlan<MT>::THREADS, MT <= 64 ? 2 : 1)
 fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const Fp8SplitArgs args) {
     using L = Fp8SplitPlan<MT>;
@@ -103,7 +123,7 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         }
         for (int b = 0; b < L::NB; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], L::EW);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -147,27 +167,32 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------- MMA issuer ---------------------------------
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int buf = i % L::NB;
-                if (!mbar_wait(&acc_empty[buf], ((i / L::NB) & 1) ^ 1, abort_flag)) { ok = false; break; }
-                if (!mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t w_addr = smem_u32(smem + L::W_OFF + stage * L::W_BYTES);
-                const uint32_t x_addr = smem_u32(smem + L::X_OFF + stage * L::X_BYTES);
+        // ------------------------------- MMA issuer ---------------------------------
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int i = 0; i < k1 - k0; ++i) {
+            const int buf = i % L::NB;
+            ok = mbar_wait_short(&acc_empty[buf], ((i / L::NB) & 1) ^ 1, abort_flag) &&
+                 mbar_wait_short(&full[stage], phase, abort_flag);
+            if (!__all_sync(kAll, ok)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t w_addr = smem_u32(smem + L::W_OFF + stage * L::W_BYTES);
+            const uint32_t x_addr = smem_u32(smem + L::X_OFF + stage * L::X_BYTES);
+            if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     tc_mma_fp8(tmem + buf * MT, sdesc_sw128(w_addr + j * 32), sdesc_sw128(x_addr + j * 32), IDESC,
                                j > 0 ? 1u : 0u);
-                tc_commit(&empty[stage]);
                 tc_commit(&acc_full[buf]);
-                if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
+                tc_commit(&empty[stage]);
             }
-            if (!ok || *abort_flag) {
+            __syncwarp();
+            if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok || *abort_flag) {
+            // Wait for the MMAs already issued before TMEM is released.
+            if (elect_one()) {
                 tc_commit(drain);
                 mbar_wait(drain, 0, nullptr);
             }
@@ -175,54 +200,53 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         __syncwarp();
     } else {
         // ------------------------------- promotion -----------------------------------
+        constexpr int ET = 32 * L::EW;
         const int q = warp & 3;
-        const int et = threadIdx.x - 64;              // 0..127
+        const int et = threadIdx.x - 64;              // 0..ET - 1
+        const int cb = (warp - 2) / 4 * L::COLS;      // this warp's first token column
         const int nl = q * 32 + lane;                 // weight row within the tile = TMEM lane
-        const int n = n_blk * 128 + nl;               // output column
         const uint32_t lane_off = (uint32_t)(q * 32) << 16;
         float* sc = reinterpret_cast<float*>(smem + L::SC_OFF);
         grid_dependency_wait();
         const float* sb = args.b_scale + (int64_t)n_blk * args.kblocks;
-        const float bias_v = (args.bias != nullptr && n < args.N) ? __uint_as_float((uint32_t)__ldg(args.bias + n) << 16)
-                                                                  : 0.0f;
-        // the scale products of a chunk of K blocks: MT x CH values over 128 threads
-        constexpr int PER = MT * CH / 128;
+        // the scale products of a chunk of K blocks: MT x CH values over ET threads
+        constexpr int PER = MT * CH / ET;
         float pre[PER];
         auto fetch = [&](int kc) {
 #pragma unroll
             for (int v = 0; v < PER; ++v) {
-                const int idx = v * 128 + et, m = m0 + idx % MT, kb = kc + idx / MT;
+                const int idx = v * ET + et, m = m0 + idx % MT, kb = kc + idx / MT;
                 pre[v] = (m < args.M && kb < k1)
                              ? __ldg(args.a_scale + m * args.stride_am + kb * args.stride_ak) * __ldg(sb + kb) : 0.0f;
             }
         };
-        float acc[MT];
+        float acc[L::COLS];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m] = 0.0f;
+        for (int m = 0; m < L::COLS; ++m) acc[m] = 0.0f;
         bool ok = true;
         fetch(k0);
         for (int kc = k0, ci = 0; kc < k1; kc += CH, ++ci) {
             // this buffer was last read two chunks ago, before every thread's previous barrier
             float* cur = sc + (ci & 1) * CH * MT;
 #pragma unroll
-            for (int v = 0; v < PER; ++v) cur[v * 128 + et] = pre[v];
-            named_barrier_sync(kSplitScaleBarrier, 128);
-            fetch(kc + CH);
+            for (int v = 0; v < PER; ++v) cur[v * ET + et] = pre[v];
+            named_barrier_sync(kSplitScaleBarrier, ET);
+            if (kc + CH < k1) fetch(kc + CH);
             const int ke = min(CH, k1 - kc);
             for (int j = 0; j < ke; ++j) {
                 const int i = kc - k0 + j, buf = i % L::NB;
-                if (ok) ok = __all_sync(kAll, mbar_wait(&acc_full[buf], (i / L::NB) & 1, abort_flag));
+                if (ok) ok = __all_sync(kAll, mbar_wait_short(&acc_full[buf], (i / L::NB) & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                const float4* s4 = reinterpret_cast<const float4*>(cur + j * MT);
+                const float4* s4 = reinterpret_cast<const float4*>(cur + j * MT + cb);
                 constexpr int W = MT < 32 ? 16 : 32;   // columns per read
 #pragma unroll
-                for (int c = 0; c < MT; c += W) {
+                for (int c = 0; c < L::COLS; c += W) {
                     uint32_t p[W];
-                    if constexpr (W == 32) tmem_load_32(tmem + lane_off + buf * MT + c, p);
-                    else tmem_load_16(tmem + lane_off + buf * MT + c, p);
+                    if constexpr (W == 32) tmem_load_32(tmem + lane_off + buf * MT + cb + c, p);
+                    else tmem_load_16(tmem + lane_off + buf * MT + cb + c, p);
                     tmem_load_wait();
-                    if (c + W == MT) {
+                    if (c + W == L::COLS) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&acc_empty[buf]);
@@ -230,52 +254,68 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
 #pragma unroll
                     for (int m = 0; m < W; m += 4) {
                         const float4 s = s4[(c + m) / 4];
-                        acc[c + m] = fmaf(s.x, __uint_as_float(p[m]), acc[c + m]);
-                        acc[c + m + 1] = fmaf(s.y, __uint_as_float(p[m + 1]), acc[c + m + 1]);
-                        acc[c + m + 2] = fmaf(s.z, __uint_as_float(p[m + 2]), acc[c + m + 2]);
-                        acc[c + m + 3] = fmaf(s.w, __uint_as_float(p[m + 3]), acc[c + m + 3]);
+                        fma2_pair(acc[c + m], acc[c + m + 1], p[m], p[m + 1], s.x, s.y);
+                        fma2_pair(acc[c + m + 2], acc[c + m + 3], p[m + 2], p[m + 3], s.z, s.w);
                     }
                 }
             }
         }
-        if (!clustered) {
-            if (ok && n < args.N) {
+        // The sums go through shared memory ([MT][128], in the place of the ring: the last acc_full says
+        // that every MMA has read it), so that the code from here on is short loops: unrolled over the
+        // registers it was fetched cold by every CTA, and that took longer than the product.
+        float* part = reinterpret_cast<float*>(smem);
+        if (ok) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    if (m0 + m < args.M)
-                        store_out_one<OT>(args.out, (int64_t)(m0 + m) * args.N + n,
-                                          args.bias != nullptr ? __fadd_rn(acc[m], bias_v) : acc[m]);
-            }
+            for (int m = 0; m < L::COLS; ++m) part[(cb + m) * 128 + nl] = acc[m];
+        }
+        if (clustered) {
+            cluster_arrive();
+            cluster_wait();
         } else {
-            // every CTA's MMAs have read their ring: its memory takes the partial sums now
-            float* part = reinterpret_cast<float*>(smem);
-            const int cw = (MT + S - 1) / S;              // columns per owner, at most
-            cluster_arrive();
-            cluster_wait();
-            int r = 0, c0 = 0, c1 = MT / S;               // owner r has the columns [MT r / S, MT (r + 1) / S)
-            uint32_t dst = map_to_rank(smem_u32(part + (size_t)rank * cw * 128 + nl), 0);
+            named_barrier_sync(kSplitScaleBarrier, ET);
+        }
+        // this CTA's token columns, four weight rows per thread at a time
+        const int b0 = MT * (int)rank / S, b1 = min(MT * ((int)rank + 1) / S, args.M - m0);
+        const int n0 = n_blk * 128 + lane * 4;
+        const bool vec = args.vec_out && n0 + 4 <= args.N;
+        float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (args.bias != nullptr) {
+            float* bv = reinterpret_cast<float*>(&bias);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                while (m >= c1) {
-                    ++r;
-                    c0 = c1;
-                    c1 = MT * (r + 1) / S;
-                    dst = map_to_rank(smem_u32(part + (size_t)rank * cw * 128 + nl), (uint32_t)r);
+            for (int e = 0; e < 4; ++e)
+                if (n0 + e < args.N) bv[e] = __uint_as_float((uint32_t)__ldg(args.bias + n0 + e) << 16);
+        }
+        for (int m = b0 + et / 32; m < b1; m += L::EW) {
+            float4 v;
+            if (clustered) {
+                const uint32_t src = smem_u32(part + m * 128 + lane * 4);
+                v = ld_cluster_v4(map_to_rank(src, 0));
+                for (int p = 1; p < S; ++p) {
+                    const float4 w = ld_cluster_v4(map_to_rank(src, (uint32_t)p));
+                    v = make_float4(__fadd_rn(v.x, w.x), __fadd_rn(v.y, w.y), __fadd_rn(v.z, w.z), __fadd_rn(v.w, w.w));
                 }
-                st_cluster_f32(dst + (uint32_t)(m - c0) * 512u, acc[m]);
+            } else {
+                v = reinterpret_cast<const float4*>(part + m * 128)[lane];
             }
+            if (args.bias != nullptr)
+                v = make_float4(__fadd_rn(v.x, bias.x), __fadd_rn(v.y, bias.y), __fadd_rn(v.z, bias.z), __fadd_rn(v.w, bias.w));
+            if (!ok) continue;
+            const int64_t at = (int64_t)(m0 + m) * args.N + n0;
+            if (vec) {
+                if constexpr (OT == OutType::FP32) *reinterpret_cast<float4*>(static_cast<float*>(args.out) + at) = v;
+                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + at) =
+                         make_uint2(pack_out2<OT>(v.x, v.y), pack_out2<OT>(v.z, v.w));
+            } else {
+                const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n0 + e < args.N) store_out_one<OT>(args.out, at + e, y[e]);
+            }
+        }
+        if (clustered) {
+            // no CTA leaves while another may still read its sums
             cluster_arrive();
             cluster_wait();
-            const int b0 = MT * (int)rank / S, b1 = MT * ((int)rank + 1) / S;
-            if (ok && n < args.N) {
-                for (int m = b0; m < b1 && m0 + m < args.M; ++m) {
-                    const float* src = part + (size_t)(m - b0) * 128 + nl;
-                    float v = src[0];
-                    for (int p = 1; p < S; ++p) v = __fadd_rn(v, src[(size_t)p * cw * 128]);
-                    if (args.bias != nullptr) v = __fadd_rn(v, bias_v);
-                    store_out_one<OT>(args.out, (int64_t)(m0 + m) * args.N + n, v);
-                }
-            }
         }
     }
     if (clustered && warp < 2) {
