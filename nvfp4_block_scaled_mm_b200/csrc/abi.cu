@@ -832,25 +832,22 @@ struct Fp8Plan {
     int mt, splits;          // the split-K kernel's token tile and cluster size
 };
 
-// The kernel of a shape, by estimated time in units of one K block of a 128 x 128 tile on one SM.
+// The kernel of a shape.  Split-K kernel: the token tile is the smallest that holds M (128 from 65 rows on);
+// K is split over clusters of a power of two of CTAs (3, 5, 6 and 7 measured slower than the power below:
+// clusters of those sizes fill the GPU's processor clusters badly) while all CTAs are resident at once (a
+// second wave always lost: 64 x 8192 x 4096 12.2 us with 4-way clusters, 19.4 with 5) and either SMs are free or
+// a CTA still has 16 blocks to stream (16 x 4096 x 4096: 7.0 us 4-way, 7.4 8-way; 16 x 4096 x 14336: 14.3 and 13.2).
+// Where 128-token tiles leave no SM free for a split, the SM-pair kernel is as fast or faster (300 x 4096 x
+// 4096: 19.1 us against 20.2; 200 x 4096 x 4096 splits 2-way: 15.1 against 18.9; 512 x 14336 x 4096: 36 against 78).
 Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t kblocks, int sms) {
-    Fp8Plan best{false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1};
-    const int64_t tiles = (N + 127) / 128 * ((M + best.mt - 1) / best.mt);
-    double best_cost = 1e30;
-    for (int s = 1; s <= kSplitMaxS && s <= kblocks; ++s) {
-        const int64_t per_sm = (tiles * s + sms - 1) / sms;
-        const double cost = (double)per_sm * ((kblocks + s - 1) / s) + (s > 1 ? 4 : 0);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best.splits = s;
-        }
-    }
-    if (M > 128) {
-        const int64_t pairs = (M + kFp8TileM - 1) / kFp8TileM * ((N + kFp8TileN - 1) / kFp8TileN);
-        const double cost = (double)((pairs + sms / 2 - 1) / (sms / 2)) * kblocks * 1.2;
-        best.pair = cost < best_cost;
-    }
-    return best;
+    Fp8Plan p{false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1};
+    const int64_t tiles = (N + 127) / 128 * ((M + p.mt - 1) / p.mt);
+    const int64_t slots = p.mt <= 64 ? 2 * (int64_t)sms : sms;
+    while (2 * p.splits <= kSplitMaxS && 2 * p.splits <= kblocks && 2 * p.splits * tiles <= slots &&
+           (2 * p.splits * tiles <= sms || kblocks / p.splits >= 16))
+        p.splits *= 2;
+    p.pair = p.mt == 128 && p.splits == 1;
+    return p;
 }
 
 template <OutType OT>

@@ -25,6 +25,7 @@ namespace nvfp4lora {
 
 constexpr int kSplitMaxS = 8;
 constexpr int kSplitScaleChunk = 8;      // K blocks whose scale products are staged at a time
+constexpr int kSplitIssuers = 2;         // MMA-issuing warps
 
 struct Fp8SplitArgs {
     const float* a_scale;    // element (m, kb) at m * stride_am + kb * stride_ak
@@ -41,10 +42,10 @@ struct Fp8SplitPlan {
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int X_BYTES = MT * 128;
     // MT <= 64: two CTAs per SM (shared memory, registers and TMEM allow both)
-    static constexpr int STAGES = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 4 : 6;
-    // promotion warps: one per TMEM lane quarter, and two for 128 columns (64 sums per thread)
-    static constexpr int EW = MT == 128 ? 8 : 4;
-    static constexpr int THREADS = 64 + 32 * EW;                      // warp 0: producer, 1: MMA issuer
+    static constexpr int STAGES = MT == 16 ? 6 : MT == 32 ? 4 : MT == 64 ? 4 : 6;
+    // promotion warps: one per TMEM lane quarter, two from 64 token columns on
+    static constexpr int EW = MT >= 64 ? 8 : 4;
+    static constexpr int THREADS = 96 + 32 * EW;                      // warp 0: producer, 1 and 2: MMA issuers
     static constexpr int COLS = MT * 4 / EW;                          // token columns per promotion thread
     static constexpr int NB = MT <= 32 ? 8 : MT == 64 ? 4 : 2;        // accumulators
     static constexpr int TMEM_COLS = NB * MT;                         // 128 or 256: a power of two
@@ -52,12 +53,15 @@ struct Fp8SplitPlan {
     static constexpr int X_OFF = W_OFF + STAGES * W_BYTES;
     static constexpr int SC_OFF = X_OFF + STAGES * X_BYTES;           // [2][chunk][MT] scale products
     static constexpr int BAR_OFF = SC_OFF + 2 * kSplitScaleChunk * MT * 4;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * NB + 1;          // full, empty, acc_full, acc_empty, drain
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * NB + kSplitIssuers;   // full, empty, acc_full, acc_empty, drain
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int TOTAL = MISC_OFF + 16;
     static constexpr int DYN_BYTES = TOTAL + 1024;
     // the finished sums take the ring's place: [MT][128] floats
     static_assert(MT * 128 * 4 <= STAGES * (W_BYTES + X_BYTES), "partials exceed the ring");
+    // a barrier's phases are all waited for by one issuer: a second one could be a whole phase ahead, where
+    // the parity it waits for is that of the phase before
+    static_assert(STAGES % kSplitIssuers == 0 && NB % kSplitIssuers == 0, "issuers must divide stages and accumulators");
     static_assert(X_BYTES % 1024 == 0, "token tiles must stay 1024-byte aligned");
     static_assert(DYN_BYTES <= (MT <= 64 ? 113 * 1024 : 227 * 1024), "split-K shared-memory plan too large");
 };
@@ -125,7 +129,7 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], L::EW);
         }
-        mbar_init(drain, 1);
+        for (int k = 0; k < kSplitIssuers; ++k) mbar_init(&drain[k], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -141,40 +145,49 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     grid_launch_dependents();
 
     if (warp == 0) {
+        // ------------------------------- TMA producer -------------------------------
+        // The ring's first fill is issued by a lane per stage (one lane alone takes about 340 cycles per
+        // stage); lane 0 refills the stages as they are handed back.  A prefetch changes no data and L2 is
+        // where device memory is kept coherent, so the weights of the first fill are warmed before the
+        // dependency wait.
+        const int mine = k0 + lane;
+        const bool first = lane < L::STAGES && mine < k1;
+        if (first) tma_prefetch_l2_2d(&tm_b, mine * 128, n_blk * 128);
+        grid_dependency_wait();
+        if (first) {
+            mbar_arrive_expect_tx(&full[lane], L::W_BYTES + L::X_BYTES);
+            tma_load_2d(smem + L::W_OFF + lane * L::W_BYTES, &tm_b, &full[lane], mine * 128, n_blk * 128);
+            tma_load_2d(smem + L::X_OFF + lane * L::X_BYTES, &tm_a, &full[lane], mine * 128, m0);
+        }
+        __syncwarp();
         if (lane == 0) {
-            // ------------------------------- TMA producer -------------------------------
-            // A prefetch changes no data and L2 is where device memory is kept coherent, so the weights
-            // of the ring's first fill may be warmed before the dependency wait.
-            for (int kb = k0; kb < min(k1, k0 + L::STAGES); ++kb) tma_prefetch_l2_2d(&tm_b, kb * 128, n_blk * 128);
-            grid_dependency_wait();
             int stage = 0;
-            uint32_t phase = 0, filled = 0, filled_parity = 0;
+            uint32_t phase = 0;
             bool ok = true;
-            for (int kb = k0; kb < k1; ++kb) {
-                if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+            for (int kb = k0 + L::STAGES; kb < k1; ++kb) {
+                if (!mbar_wait_short(&empty[stage], phase, abort_flag)) { ok = false; break; }
                 mbar_arrive_expect_tx(&full[stage], L::W_BYTES + L::X_BYTES);
                 tma_load_2d(smem + L::W_OFF + stage * L::W_BYTES, &tm_b, &full[stage], kb * 128, n_blk * 128);
                 tma_load_2d(smem + L::X_OFF + stage * L::X_BYTES, &tm_a, &full[stage], kb * 128, m0);
-                filled |= 1u << stage;
-                filled_parity = (filled_parity & ~(1u << stage)) | (phase << stage);
                 if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
             }
             if (!ok || *abort_flag) {
-                // Let the copies already issued land before the CTA can exit.
+                // Let the copies already issued land before the CTA can exit: the stages before `stage` were
+                // filled in this round too, with the other parity.
                 for (int s = 0; s < L::STAGES; ++s)
-                    if ((filled >> s) & 1u) mbar_wait(&full[s], (filled_parity >> s) & 1u, nullptr);
+                    if (k0 + s < k1) mbar_wait(&full[s], s < stage ? phase ^ 1 : phase, nullptr);
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------- MMA issuer ---------------------------------
-        int stage = 0;
-        uint32_t phase = 0;
+    } else if (warp <= kSplitIssuers) {
+        // ------------------------------- MMA issuers ---------------------------------
+        // The blocks in turn: one warp's waits, vote and issue take about 700 cycles per block, more than
+        // the block's MMAs or its share of the weight stream.
         bool ok = true;
-        for (int i = 0; i < k1 - k0; ++i) {
-            const int buf = i % L::NB;
-            ok = mbar_wait_short(&acc_empty[buf], ((i / L::NB) & 1) ^ 1, abort_flag) &&
-                 mbar_wait_short(&full[stage], phase, abort_flag);
+        for (int i = warp - 1; i < k1 - k0; i += kSplitIssuers) {
+            const int buf = i % L::NB, stage = i % L::STAGES;
+            ok = mbar_wait_short(&full[stage], (i / L::STAGES) & 1, abort_flag) &&
+                 (i < L::NB || mbar_wait_short(&acc_empty[buf], ((i / L::NB) & 1) ^ 1, abort_flag));
             if (!__all_sync(kAll, ok)) { ok = false; break; }
             tc_fence_after();
             const uint32_t w_addr = smem_u32(smem + L::W_OFF + stage * L::W_BYTES);
@@ -185,16 +198,15 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                     tc_mma_fp8(tmem + buf * MT, sdesc_sw128(w_addr + j * 32), sdesc_sw128(x_addr + j * 32), IDESC,
                                j > 0 ? 1u : 0u);
                 tc_commit(&acc_full[buf]);
-                tc_commit(&empty[stage]);
+                if (i + L::STAGES < k1 - k0) tc_commit(&empty[stage]);
             }
             __syncwarp();
-            if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
         }
         if (!ok || *abort_flag) {
             // Wait for the MMAs already issued before TMEM is released.
             if (elect_one()) {
-                tc_commit(drain);
-                mbar_wait(drain, 0, nullptr);
+                tc_commit(&drain[warp - 1]);
+                mbar_wait(&drain[warp - 1], 0, nullptr);
             }
         }
         __syncwarp();
@@ -202,22 +214,24 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         // ------------------------------- promotion -----------------------------------
         constexpr int ET = 32 * L::EW;
         const int q = warp & 3;
-        const int et = threadIdx.x - 64;              // 0..ET - 1
-        const int cb = (warp - 2) / 4 * L::COLS;      // this warp's first token column
+        const int et = threadIdx.x - 96;              // 0..ET - 1
+        const int cb = (warp - 3) / 4 * L::COLS;      // this warp's first token column
         const int nl = q * 32 + lane;                 // weight row within the tile = TMEM lane
         const uint32_t lane_off = (uint32_t)(q * 32) << 16;
         float* sc = reinterpret_cast<float*>(smem + L::SC_OFF);
         grid_dependency_wait();
         const float* sb = args.b_scale + (int64_t)n_blk * args.kblocks;
-        // the scale products of a chunk of K blocks: MT x CH values over ET threads
+        // the scales of a chunk of K blocks: MT x CH products over ET threads, loaded a chunk ahead and
+        // multiplied when they are staged (a multiply at the load would stall the warp on it)
         constexpr int PER = MT * CH / ET;
-        float pre[PER];
+        float pre_a[PER], pre_b[PER];
         auto fetch = [&](int kc) {
 #pragma unroll
             for (int v = 0; v < PER; ++v) {
                 const int idx = v * ET + et, m = m0 + idx % MT, kb = kc + idx / MT;
-                pre[v] = (m < args.M && kb < k1)
-                             ? __ldg(args.a_scale + m * args.stride_am + kb * args.stride_ak) * __ldg(sb + kb) : 0.0f;
+                const bool in = m < args.M && kb < k1;
+                pre_a[v] = in ? __ldg(args.a_scale + m * args.stride_am + kb * args.stride_ak) : 0.0f;
+                pre_b[v] = in ? __ldg(sb + kb) : 0.0f;
             }
         };
         float acc[L::COLS];
@@ -229,7 +243,7 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             // this buffer was last read two chunks ago, before every thread's previous barrier
             float* cur = sc + (ci & 1) * CH * MT;
 #pragma unroll
-            for (int v = 0; v < PER; ++v) cur[v * ET + et] = pre[v];
+            for (int v = 0; v < PER; ++v) cur[v * ET + et] = pre_a[v] * pre_b[v];
             named_barrier_sync(kSplitScaleBarrier, ET);
             if (kc + CH < k1) fetch(kc + CH);
             const int ke = min(CH, k1 - kc);
@@ -239,7 +253,7 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 if (!ok) break;
                 tc_fence_after();
                 const float4* s4 = reinterpret_cast<const float4*>(cur + j * MT + cb);
-                constexpr int W = MT < 32 ? 16 : 32;   // columns per read
+                constexpr int W = L::COLS < 32 || MT == 64 ? 16 : 32;   // columns per read
 #pragma unroll
                 for (int c = 0; c < L::COLS; c += W) {
                     uint32_t p[W];
@@ -289,11 +303,17 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             float4 v;
             if (clustered) {
                 const uint32_t src = smem_u32(part + m * 128 + lane * 4);
-                v = ld_cluster_v4(map_to_rank(src, 0));
-                for (int p = 1; p < S; ++p) {
-                    const float4 w = ld_cluster_v4(map_to_rank(src, (uint32_t)p));
-                    v = make_float4(__fadd_rn(v.x, w.x), __fadd_rn(v.y, w.y), __fadd_rn(v.z, w.z), __fadd_rn(v.w, w.w));
-                }
+                // all reads are on their way before the first addition; rank order whatever S is
+                float4 w[kSplitMaxS];
+#pragma unroll
+                for (int p = 0; p < kSplitMaxS; ++p)
+                    if (p < S) w[p] = ld_cluster_v4(map_to_rank(src, (uint32_t)p));
+                v = w[0];
+#pragma unroll
+                for (int p = 1; p < kSplitMaxS; ++p)
+                    if (p < S)
+                        v = make_float4(__fadd_rn(v.x, w[p].x), __fadd_rn(v.y, w[p].y), __fadd_rn(v.z, w[p].z),
+                                        __fadd_rn(v.w, w[p].w));
             } else {
                 v = reinterpret_cast<const float4*>(part + m * 128)[lane];
             }
@@ -318,7 +338,7 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             cluster_wait();
         }
     }
-    if (clustered && warp < 2) {
+    if (clustered && warp < 3) {
         // one arrive / wait pair per thread for each of the two meetings above
         cluster_arrive();
         cluster_wait();
