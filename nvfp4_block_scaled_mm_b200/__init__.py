@@ -109,7 +109,9 @@ class _LazyLib:
     def __getattr__(self, name):
         if _LazyLib._handle is None:
             _LazyLib._handle = _load()
-        return getattr(_LazyLib._handle, name)
+        value = getattr(_LazyLib._handle, name)
+        self.__dict__[name] = value
+        return value
 
 
 _lib = _LazyLib()
@@ -316,8 +318,9 @@ def _same_device(anchor_name: str, anchor: torch.Tensor, **others) -> None:
     and read every operand by address there, so an operand on another GPU would be read through
     a foreign address.  ValueError names the first tensor that differs (None entries are
     skipped)."""
+    device = anchor.device
     for name, t in others.items():
-        if t is not None and t.device != anchor.device:
+        if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device} but {anchor_name} is on {anchor.device}: "
                              "every tensor of a call must be on the same device")
 
@@ -637,21 +640,21 @@ _SELF_COUNT_SLOTS = 16384      # more slots than this take a workspace
 _COUNT_CHUNKS = 64
 
 
-class _Here:
-    """Stands in for ``torch.cuda.device`` where the tensors' device is the current one already."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
+# The current stream's handle without building a Stream object (2.3 us less per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-_HERE = _Here()
-
-
-def _on_device(device: torch.device):
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _call(fn, device: torch.device, *args) -> None:
+    """Run a C entry point on the current stream of the tensors' device (the last argument it takes)."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != OK:
+        _check(status)
 
 
 class MoePermutation(NamedTuple):
@@ -680,20 +683,16 @@ def _need_row_dtype(t, name):
 
 def _moe_permute(x, topk_ids, num_experts, align, zero_padding, out):
     T, top_k = topk_ids.shape
-    dev = x.device
     capacity = out.shape[0]
-    with _on_device(dev):
-        n = T * top_k
-        # one allocation for the tables; the row -> slot table starts on a 16-byte boundary
-        a, b = -(-(num_experts + 1) // 4) * 4, -(-n // 4) * 4
-        ws = _COUNT_CHUNKS * num_experts if n > _SELF_COUNT_SLOTS else 0
-        tables = torch.empty(a + b + capacity, dtype=torch.int32, device=dev)
-        m_indptr = tables[:num_experts + 1]
-        idx = tables[a:a + n].view(T, top_k)
-        inv = tables[a + b:]
-        work = torch.empty(ws, dtype=torch.int32, device=dev) if ws else None
-        nvfp4lora_moe_permute(x, T, x.shape[1] * x.element_size(), topk_ids, top_k, num_experts, align, zero_padding,
-                              out, capacity, m_indptr, idx, inv, work, 4 * ws, torch.cuda.current_stream(dev))
+    n = T * top_k
+    m_indptr = topk_ids.new_empty(num_experts + 1)
+    idx = torch.empty_like(topk_ids)
+    inv = topk_ids.new_empty(capacity)
+    work = topk_ids.new_empty(_COUNT_CHUNKS * num_experts) if n > _SELF_COUNT_SLOTS else None
+    _call(_lib.nvfp4lora_moe_permute, x.device, x.data_ptr(), T, x.shape[1] * x.element_size(), topk_ids.data_ptr(),
+          top_k, num_experts, align, 1 if zero_padding else 0, out.data_ptr(), capacity, m_indptr.data_ptr(),
+          idx.data_ptr(), inv.data_ptr(), None if work is None else work.data_ptr(),
+          0 if work is None else 4 * work.numel())
     return out, m_indptr, idx, inv
 
 
@@ -785,15 +784,14 @@ def _moe_unpermute(y, idx, topk_weights, out, name="y"):
         if topk_weights.shape != idx.shape:
             raise ValueError(f"topk_weights must be [T, top_k] = {tuple(idx.shape)}, got {tuple(topk_weights.shape)}")
     if out is None:
-        out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+        out = y.new_empty((T, H))
     else:
         _need(out, "out", y.dtype, 2)
         if tuple(out.shape) != (T, H):
             raise ValueError(f"out must be [T, H] = [{T}, {H}], got {tuple(out.shape)}")
     _same_device(name, y, expanded_idx_to_permuted_idx=idx, topk_weights=topk_weights, out=out)
-    with _on_device(y.device):
-        nvfp4lora_moe_unpermute(y, y.shape[0], H, _ROW_DTYPES[y.dtype], idx, topk_weights, T, top_k, out,
-                                torch.cuda.current_stream(y.device))
+    _call(_lib.nvfp4lora_moe_unpermute, y.device, y.data_ptr(), y.shape[0], H, _ROW_DTYPES[y.dtype], idx.data_ptr(),
+          None if topk_weights is None else topk_weights.data_ptr(), T, top_k, out.data_ptr())
     return out
 
 
@@ -878,11 +876,10 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
             raise ValueError(f"grad_rows must be [rows, H] = [{rows}, {H}], got {tuple(grad_rows.shape)}")
     _same_device("grad_out", grad_out, y=y, expanded_idx_to_permuted_idx=idx, permuted_idx_to_expanded_idx=inv,
                  m_indptr=m_indptr, topk_weights=topk_weights, grad_rows=grad_rows)
-    with _on_device(grad_out.device):
-        nvfp4lora_moe_unpermute_backward(grad_out, y if topk_weights is not None else None, rows, H,
-                                         _ROW_DTYPES[grad_out.dtype], idx, inv, m_indptr, m_indptr.shape[0] - 1,
-                                         topk_weights, T, top_k, grad_rows, grad_weights,
-                                         torch.cuda.current_stream(grad_out.device))
+    _call(_lib.nvfp4lora_moe_unpermute_backward, grad_out.device, grad_out.data_ptr(),
+          None if topk_weights is None else y.data_ptr(), rows, H, _ROW_DTYPES[grad_out.dtype], idx.data_ptr(),
+          inv.data_ptr(), m_indptr.data_ptr(), m_indptr.shape[0] - 1, _ptr(topk_weights), T, top_k,
+          grad_rows.data_ptr(), _ptr(grad_weights))
     return grad_rows, grad_weights
 
 
@@ -894,7 +891,7 @@ def _fp8_outputs(x, block_rows, q, scales):
     rows, H = x.shape
     shape = (-(-rows // block_rows), -(-H // 128))
     if q is None:
-        q = torch.empty((rows, H), dtype=torch.float8_e4m3fn, device=x.device)
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     else:
         _need(q, "q", torch.float8_e4m3fn, 2)
         if tuple(q.shape) != (rows, H):
@@ -902,7 +899,7 @@ def _fp8_outputs(x, block_rows, q, scales):
     if scales is None:
         # activations' scales column-major: the product reads consecutive rows' scales together
         strides = (1, shape[0]) if block_rows == 1 else (shape[1], 1)
-        scales = torch.empty_strided(shape, strides, dtype=torch.float32, device=x.device)
+        scales = x.new_empty_strided(shape, strides, dtype=torch.float32)
     elif (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or not scales.is_cuda
           or tuple(scales.shape) != shape):
         raise ValueError(f"scales must be a float32 CUDA tensor of shape {shape}")
@@ -924,10 +921,10 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
         raise ValueError(f"block_rows = {block_rows}: 1 or 128 is required")
     q, scales = _fp8_outputs(x, block_rows, q, scales)
     _same_device("x", x, q=q, scales=scales)
+    rows, H = x.shape
     sr, sg = scales.stride()
-    with _on_device(x.device):
-        nvfp4lora_fp8_quantize(x, x.shape[0], x.shape[1], _ROW_DTYPES[x.dtype], block_rows, q, scales, sr, sg,
-                               torch.cuda.current_stream(x.device))
+    _call(_lib.nvfp4lora_fp8_quantize, x.device, x.data_ptr(), rows, H, _ROW_DTYPES[x.dtype], block_rows, q.data_ptr(),
+          scales.data_ptr(), sr, sg)
     return q, scales
 
 
@@ -955,9 +952,8 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
     q, scales = _fp8_outputs(x, 1, q, scales)
     _same_device("x", x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
     sr, sg = scales.stride()
-    with _on_device(x.device):
-        nvfp4lora_rmsnorm_fp8_quantize(x, residual, weight, x.shape[0], H, _ROW_DTYPES[x.dtype], eps, norm_out, q,
-                                       scales, sr, sg, torch.cuda.current_stream(x.device))
+    _call(_lib.nvfp4lora_rmsnorm_fp8_quantize, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), x.shape[0], H,
+          _ROW_DTYPES[x.dtype], eps, _ptr(norm_out), q.data_ptr(), scales.data_ptr(), sr, sg)
     return q, scales
 
 
@@ -993,14 +989,13 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
     if out_dtype not in _ROW_DTYPES:
         raise ValueError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = a.new_empty((M, N), dtype=out_dtype)
     else:
         _need(out, "out", out_dtype, 2)
         if tuple(out.shape) != (M, N):
             raise ValueError(f"out must be [M, N] = [{M}, {N}]")
     _same_device("a", a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
     sm, sk = a_scale.stride()
-    with _on_device(a.device):
-        nvfp4lora_mm_fp8(a, b, a_scale, sm, sk, b_scale, bias, out, _ROW_DTYPES[out_dtype], M, N, K,
-                         torch.cuda.current_stream(a.device))
+    _call(_lib.nvfp4lora_mm_fp8, a.device, a.data_ptr(), b.data_ptr(), a_scale.data_ptr(), sm, sk, b_scale.data_ptr(),
+          _ptr(bias), out.data_ptr(), _ROW_DTYPES[out_dtype], M, N, K)
     return out
