@@ -310,7 +310,7 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_bgmv_moe_gemm2_lora_delta(
  *            floor((n + min(num_experts, n) * (align - 1)) / align) * align with n = num_tokens * top_k.
  *   m_indptr int32 [num_experts + 1]; expanded_idx_to_permuted_idx int32 [num_tokens * top_k];
  *   permuted_idx_to_expanded_idx int32 [padded_rows].
- *   workspace  4 * 64 * num_experts bytes when num_tokens * top_k > 16384 (else ignored, may be NULL);
+ *   workspace  4 * 64 * num_experts bytes when num_tokens * top_k > 4096 (else ignored, may be NULL);
  *            its contents need not be kept; two calls that may run at once need two.
  * Rules: 1 <= top_k <= 16, 1 <= num_experts <= 1024, 1 <= align <= 4096, num_tokens >= 0 (0 writes an
  * all-zero m_indptr and -1 entries).  Read on the device only: graph-capturable.  An expert id

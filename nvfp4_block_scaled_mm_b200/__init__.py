@@ -636,7 +636,7 @@ def fp4_quantize(x: torch.Tensor, global_scale: torch.Tensor, *, codes: Optional
 # --------------------------------------------------------------------------------------
 
 _ROW_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_SELF_COUNT_SLOTS = 16384      # more slots than this take a workspace
+_SELF_COUNT_SLOTS = 4096      # more slots than this take a workspace
 _COUNT_CHUNKS = 64
 
 

@@ -690,7 +690,7 @@ nvfp4lora_status launch_dependent(const char* what, Kernel kernel, int64_t grid,
 }
 
 // Slots up to which every CTA of the permute kernel counts all of them itself (one launch).
-constexpr int64_t kMoeSelfCountSlots = 16384;
+constexpr int64_t kMoeSelfCountSlots = 4096;
 
 nvfp4lora_status check_routing(int64_t T, int64_t top_k, int64_t rows) {
     if (T < 0 || T > kMaxDim) return fail(NVFP4LORA_ERR_INVALID_ARG, "num_tokens = %lld out of range", (long long)T);
@@ -1291,7 +1291,7 @@ nvfp4lora_status nvfp4lora_moe_permute(const void* x, int64_t num_tokens, int64_
     // a token per CTA at least, or about eight padding rows; four CTAs per SM at most
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(num_tokens, padded_rows / 8),
                                                                 (int64_t)info->sms * 4));
-    auto go = [&](auto kernel) { return launch_dependent("permute launch", kernel, grid, kMoeThreads, s, a); };
+    auto go = [&](auto kernel) { return launch_dependent("permute launch", kernel, grid, kMoePermuteThreads, s, a); };
     auto fits = [&](int64_t v) { return row_bytes % v == 0 && aligned(x, v) && aligned(rows, v); };
     if (fits(16)) return go(moe_permute_kernel<16>);
     if (fits(4)) return go(moe_permute_kernel<4>);
@@ -1322,18 +1322,17 @@ nvfp4lora_status nvfp4lora_moe_unpermute(const void* y, int64_t padded_rows, int
     a.idx = expanded_idx_to_permuted_idx;
     a.w = topk_weights;
     a.out = out;
-    a.nv = vec ? H * es / 16 : H;
-    a.segs = (int)((a.nv + 31) / 32);
+    a.H = H;
+    a.segs = (int)((H + 255) / 256);
     a.units = num_tokens * a.segs;
     a.top_k = (int)top_k;
     a.rows = (int)padded_rows;
     const int64_t grid = (a.units + kMoeThreads / 32 - 1) / (kMoeThreads / 32);
     return by_type(dtype, [&](auto ty) {
         constexpr MoeType TY = decltype(ty)::value;
-        constexpr int VE = TY == MoeType::FP32 ? 4 : 8;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-        return vec ? launch_dependent("unpermute launch", moe_unpermute_kernel<TY, VE>, grid, kMoeThreads, s, a)
-                   : launch_dependent("unpermute launch", moe_unpermute_kernel<TY, 1>, grid, kMoeThreads, s, a);
+        return vec ? launch_dependent("unpermute launch", moe_unpermute_kernel<TY, true>, grid, kMoeThreads, s, a)
+                   : launch_dependent("unpermute launch", moe_unpermute_kernel<TY, false>, grid, kMoeThreads, s, a);
     });
 }
 
@@ -1387,19 +1386,18 @@ nvfp4lora_status nvfp4lora_moe_unpermute_backward(const void* grad_out, const vo
     a.w = topk_weights;
     a.gy = grad_rows;
     a.gw = grad_weights;
-    a.nv = vec ? H * es / 16 : H;
+    a.H = H;
     a.T = (int)num_tokens;
     a.top_k = (int)top_k;
     a.rows = (int)padded_rows;
-    const int block = (int)std::min<int64_t>(kMoeThreads, (a.nv + 31) / 32 * 32);
+    const int block = (int)std::min<int64_t>(kMoeBwdThreads, (H + 255) / 256 * 32);
     // the padding rows: up to two CTAs per SM
     const int64_t grid = num_tokens + std::min<int64_t>((padded_rows + 255) / 256, 2 * (int64_t)info->sms);
     return by_type(dtype, [&](auto ty) {
         constexpr MoeType TY = decltype(ty)::value;
-        constexpr int VE = TY == MoeType::FP32 ? 4 : 8;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-        return vec ? launch_dependent("unpermute gradient launch", moe_unpermute_bwd_kernel<TY, VE>, grid, block, s, a)
-                   : launch_dependent("unpermute gradient launch", moe_unpermute_bwd_kernel<TY, 1>, grid, block, s, a);
+        return vec ? launch_dependent("unpermute gradient launch", moe_unpermute_bwd_kernel<TY, true>, grid, block, s, a)
+                   : launch_dependent("unpermute gradient launch", moe_unpermute_bwd_kernel<TY, false>, grid, block, s, a);
     });
 }
 
@@ -1468,18 +1466,19 @@ nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(const void* x, void* residual, c
     a.H = H;
     a.eps = eps;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t nv = H / 8;
-    const bool vec = H % 8 == 0 && nv <= 4 * kNormMaxThreads && aligned(x, 16) && aligned(residual, 16) &&
-                     aligned(weight, 16) && aligned(norm_out, 16) && aligned(q, 8);
+    const bool vec = H % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) &&
+                     aligned(norm_out, 16) && aligned(q, 8);
     return by_type(dtype, [&](auto ty) {
         constexpr MoeType TY = decltype(ty)::value;
-        if (!vec) return launch_dependent("norm launch", row_fp8_kernel<TY, true>, rows, 256, s, a);
+        // longer rows than the registers of a CTA hold are read twice
+        if (H > kNormMaxThreads * 8 * 4) return launch_dependent("norm launch", row_fp8_kernel<TY, true>, rows, 256, s, a);
         auto go = [&](auto kernel, int per) {
-            return launch_dependent("norm launch", kernel, rows, (int)(((nv + per - 1) / per + 31) / 32 * 32), s, a);
+            return launch_dependent("norm launch", kernel, rows, (int)((H + 256 * per - 1) / (256 * per) * 32), s, a);
         };
-        if (nv <= 256) return go(rmsnorm_fp8_kernel<TY, 1>, 1);
-        if (nv <= 2 * kNormMaxThreads) return go(rmsnorm_fp8_kernel<TY, 2>, 2);
-        return go(rmsnorm_fp8_kernel<TY, 4>, 4);
+        if (H <= 2048) return vec ? go(rmsnorm_fp8_kernel<TY, 1, true>, 1) : go(rmsnorm_fp8_kernel<TY, 1, false>, 1);
+        if (H <= kNormMaxThreads * 8 * 2)
+            return vec ? go(rmsnorm_fp8_kernel<TY, 2, true>, 2) : go(rmsnorm_fp8_kernel<TY, 2, false>, 2);
+        return vec ? go(rmsnorm_fp8_kernel<TY, 4, true>, 4) : go(rmsnorm_fp8_kernel<TY, 4, false>, 4);
     });
 }
 

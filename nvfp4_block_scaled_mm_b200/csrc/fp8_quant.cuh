@@ -54,44 +54,14 @@ __device__ __forceinline__ float abs_max8(const float (&y)[8]) {
     return m;
 }
 
-// Eight consecutive elements as fp32 (16-byte loads; 32 bytes of fp32) and back.
-template <MoeType TY>
-struct Row8 {
-    static constexpr int NW = TY == MoeType::FP32 ? 2 : 1;
-    struct Raw { uint4 w[NW]; };
-    static __device__ __forceinline__ Raw load(const void* p, int64_t v) {
-        Raw r;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[v * NW + i];
-        return r;
-    }
-    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
-        if constexpr (TY == MoeType::FP32) memcpy(f, &r, 32);
-        else MoePack<TY, 8>::unpack(r.w[0], f);
-    }
-    static __device__ __forceinline__ void store(void* p, int64_t v, const float (&f)[8]) {
-        if constexpr (TY == MoeType::FP32) {
-            Raw r;
-            memcpy(&r, f, 32);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(p)[v * 2 + i] = r.w[i];
-        } else {
-            reinterpret_cast<uint4*>(p)[v] = MoePack<TY, 8>::pack(f);
-        }
-    }
-};
-
 template <MoeType TY>
 __device__ __forceinline__ float load_one(const void* p, int64_t i) {
-    float f[1];
-    MoePack<TY, 1>::load(p, i, f);
-    return f[0];
+    return to_f32<TY>(static_cast<const typename MoeElem<TY>::type*>(p)[i]);
 }
 
 template <MoeType TY>
 __device__ __forceinline__ void store_one(void* p, int64_t i, float y) {
-    const float f[1] = {y};
-    reinterpret_cast<typename MoePack<TY, 1>::V*>(p)[i] = MoePack<TY, 1>::pack(f);
+    static_cast<typename MoeElem<TY>::type*>(p)[i] = from_f32<TY>(y);
 }
 
 // Sum over the CTA, the same in every thread (fixed order).  `red` holds 32 floats.
@@ -107,80 +77,87 @@ __device__ __forceinline__ float cta_sum(float s, float* red) {
     return t;
 }
 
-// ---- norm: a CTA per row, the row kept in registers (NV vectors of 8 per thread) ----
-// HBM-bound: 2 + 1 bytes per element (16-bit types), and 4 more with a residual.  H % 8 == 0 and
-// 16-byte aligned rows; a 1 x 128 group is 16 neighbouring lanes.
-template <MoeType TY, int NV>
+// ---- norm: a CTA per row, the row kept in registers (NV chunks of 256 elements per warp) ----
+// HBM-bound: 2 + 1 bytes per element (16-bit types), and 4 more with a residual.  A chunk is two 1 x 128
+// groups: with VEC (aligned rows, H % 8 == 0) one per half-warp, otherwise the lanes' first and last four.
+template <MoeType TY, int NV, bool VEC>
 __global__ void __launch_bounds__(kNormMaxThreads)
 rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
-    using R = Row8<TY>;
+    using C = RowChunk<TY, VEC>;
     __shared__ float red[32];
-    const int nv = (int)(a.H / 8);
-    const int tid = threadIdx.x;
-    const int64_t base = (int64_t)blockIdx.x * nv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int64_t row = blockIdx.x, H = a.H;
+    const void* x = row_at<TY>(a.x, row, H);
+    void* res = a.residual != nullptr ? row_at<TY>(a.residual, row, H) : nullptr;
     float h[NV][8];
-    typename R::Raw wt[NV];
-    // the weight is not written by the kernels before this one on the stream in a program that keeps
-    // it, but it may be: nothing is read before the dependency wait
+    typename C::Raw wt[NV];
     grid_dependency_wait();
     grid_launch_dependents();
     float ss = 0.0f;
     {
-        typename R::Raw xr[NV], rr[NV];
+        typename C::Raw xr[NV], rr[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = tid + i * blockDim.x;
-            if (v < nv) {
-                xr[i] = R::load(a.x, base + v);
-                if (a.residual != nullptr) rr[i] = R::load(a.residual, base + v);
-                wt[i] = R::load(a.weight, v);
-            }
+            const int64_t e0 = (int64_t)(warp + i * nw) * 256;
+            xr[i] = C::load(x, e0, H, lane);
+            if (res != nullptr) rr[i] = C::load(res, e0, H, lane);
+            wt[i] = C::load(a.weight, e0, H, lane);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = tid + i * blockDim.x;
+            C::unpack(xr[i], h[i]);
+            if (res != nullptr) {
+                float r[8];
+                C::unpack(rr[i], r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
-            if (v < nv) {
-                R::unpack(xr[i], h[i]);
-                if (a.residual != nullptr) {
-                    float r[8];
-                    R::unpack(rr[i], r);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) h[i][e] += r[e];
-                    R::store(a.residual, base + v, h[i]);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+                for (int e = 0; e < 8; ++e) h[i][e] += r[e];
+                C::store(res, (int64_t)(warp + i * nw) * 256, H, lane, h[i]);
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);   // elements past H are 0
         }
     }
-    const float rms = rsqrtf(cta_sum(ss, red) / (float)a.H + a.eps);
+    const float rms = rsqrtf(cta_sum(ss, red) / (float)H + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * blockDim.x;
+        const int64_t e0 = (int64_t)(warp + i * nw) * 256;
         float y[8];
+        C::unpack(wt[i], y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-        if (v < nv) {
-            R::unpack(wt[i], y);
+        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rms * y[e];
+        float* sc = a.scales + row * a.stride_r;
+        uint8_t* q = a.q + row * H;
+        if constexpr (VEC) {
+            float m = abs_max8(y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rms * y[e];
+            for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            m = fmaxf(m, kFp8Tiny);
+            const int64_t at = e0 + lane * 8;
+            if (at < H) {
+                *reinterpret_cast<uint2*>(q + at) = e4m3x8_scaled(y, __fdiv_rn(kFp8Max, m));
+                if ((lane & 15) == 0) sc[at / 128 * a.stride_g] = __fdiv_rn(m, kFp8Max);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                float m = fmaxf(fmaxf(fabsf(y[4 * g]), fabsf(y[4 * g + 1])), fmaxf(fabsf(y[4 * g + 2]), fabsf(y[4 * g + 3])));
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                m = fmaxf(m, kFp8Tiny);
+                const float inv = __fdiv_rn(kFp8Max, m);
+#pragma unroll
+                for (int e = 4 * g; e < 4 * g + 4; ++e)
+                    if (C::at(e0, lane, e) < H) q[C::at(e0, lane, e)] = (uint8_t)e4m3x2_rn(y[e] * inv, 0.0f);
+                if (lane == 0 && e0 + g * 128 < H) sc[(e0 / 128 + g) * a.stride_g] = __fdiv_rn(m, kFp8Max);
+            }
         }
-        float m = abs_max8(y);
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        m = fmaxf(m, kFp8Tiny);
-        if (v < nv) {
-            reinterpret_cast<uint2*>(a.q)[base + v] = e4m3x8_scaled(y, __fdiv_rn(kFp8Max, m));
-            if (a.norm_out != nullptr) R::store(a.norm_out, base + v, y);
-            if ((v & 15) == 0) a.scales[blockIdx.x * a.stride_r + (v >> 4) * a.stride_g] = __fdiv_rn(m, kFp8Max);
-        }
+        if (a.norm_out != nullptr) C::store(row_at<TY>(a.norm_out, row, H), e0, H, lane, y);
     }
 }
 
-// ---- any row length and alignment: a CTA per row, a warp per group, the row read twice ----
-// NORM = false: the quantizer of x itself.
+// ---- a CTA per row, a warp per group, any row length and alignment ----
+// NORM = false: the quantizer of x itself.  NORM = true: the norm of rows longer than a CTA's registers hold,
+// which are read twice.
 template <MoeType TY, bool NORM>
 __global__ void __launch_bounds__(256)
 row_fp8_kernel(const Fp8QuantArgs a) {
@@ -238,7 +215,7 @@ row_fp8_kernel(const Fp8QuantArgs a) {
 template <MoeType TY>
 __global__ void __launch_bounds__(256)
 quantize_fp8_rows_kernel(const Fp8QuantArgs a) {
-    using R = Row8<TY>;
+    using R = RowChunk<TY, true>;
     constexpr int UN = TY == MoeType::FP32 ? 2 : 4;
     const int64_t groups = (a.H + 127) / 128;
     const int nv = (int)(a.H / 8);
@@ -260,7 +237,7 @@ quantize_fp8_rows_kernel(const Fp8QuantArgs a) {
             row[u] = g / groups;
             gr[u] = (int)(g - row[u] * groups);
             on[u] = g < total && gr[u] * 16 + hl < nv;
-            if (on[u]) raw[u] = R::load(a.x, row[u] * nv + gr[u] * 16 + hl);
+            if (on[u]) raw[u] = R::load(a.x, (row[u] * nv + gr[u] * 16 + hl) * 8, INT64_MAX, 0);
         }
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
@@ -284,7 +261,7 @@ quantize_fp8_rows_kernel(const Fp8QuantArgs a) {
 template <MoeType TY>
 __global__ void __launch_bounds__(256)
 quantize_fp8_blocks_kernel(const Fp8QuantArgs a) {
-    using R = Row8<TY>;
+    using R = RowChunk<TY, true>;
     __shared__ float red[8];
     const int nv = (int)(a.H / 8);
     const int64_t gcols = (a.H + 127) / 128;
@@ -296,7 +273,7 @@ quantize_fp8_blocks_kernel(const Fp8QuantArgs a) {
     typename R::Raw raw[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (c < nv && r0 + i * 16 < a.rows) raw[i] = R::load(a.x, (r0 + i * 16) * nv + c);
+        if (c < nv && r0 + i * 16 < a.rows) raw[i] = R::load(a.x, ((r0 + i * 16) * nv + c) * 8, INT64_MAX, 0);
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -336,6 +313,7 @@ blocks_fp8_kernel(const Fp8QuantArgs a) {
     grid_launch_dependents();
     float m = 0.0f;
     if (c < a.H)
+#pragma unroll 8
         for (int64_t r = r0; r < r1; r += 2) m = fmaxf(m, fabsf(load_one<TY>(a.x, r * a.H + c)));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
@@ -346,6 +324,7 @@ blocks_fp8_kernel(const Fp8QuantArgs a) {
     for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
     const float inv = __fdiv_rn(kFp8Max, m);
     if (c < a.H)
+#pragma unroll 8
         for (int64_t r = r0; r < r1; r += 2)
             a.q[r * a.H + c] = (uint8_t)e4m3x2_rn(load_one<TY>(a.x, r * a.H + c) * inv, 0.0f);
     if (threadIdx.x == 0) a.scales[br * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);

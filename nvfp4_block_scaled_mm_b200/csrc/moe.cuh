@@ -27,7 +27,7 @@ constexpr int kMoeThreads = 256;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxAlign = 4096;
-constexpr int kMoeBatchSlots = 512;      // slots ranked at a time by one CTA (kMoeMaxTopK at least)
+constexpr int kMoeBatchSlots = 64;       // slots ranked at a time by one CTA (kMoeMaxTopK at least)
 constexpr int kMoeCountChunks = 64;      // CTAs of the counting kernel
 constexpr int kErrBadSlot = 4;           // device error word: an expert id or row index out of range
 
@@ -71,7 +71,8 @@ template <> struct MoeVec<1> { using type = uint8_t; };
 // Exclusive prefix sums over the experts of the aligned segment sizes (offs) and of the padding
 // row counts (pads); offs[E] and pads[E] are the totals.  All threads of the CTA take part.
 __device__ __forceinline__ void moe_scan(const int32_t* total, int E, int align, int32_t* offs, int32_t* pads) {
-    __shared__ int32_t warp_seg[kMoeThreads / 32], warp_pad[kMoeThreads / 32];
+    // the first kMoeThreads threads hold PER experts each; further warps hold none
+    __shared__ int32_t warp_seg[32], warp_pad[32];
     constexpr int PER = kMoeMaxExperts / kMoeThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int32_t seg[PER], pad[PER], s = 0, p = 0;
@@ -100,28 +101,30 @@ __device__ __forceinline__ void moe_scan(const int32_t* total, int E, int align,
         const int e = tid * PER + q;
         if (e <= E) { offs[e] = bs + seg[q]; pads[e] = bp + pad[q]; }
     }
-    // E = kMoeMaxExperts: entry E lies past the last thread's experts
-    if (tid == kMoeThreads - 1 && E == kMoeMaxExperts) { offs[E] = bs + s; pads[E] = bp + p; }
     __syncthreads();
 }
 
 // CTA c owns the tokens [T c / grid, T (c + 1) / grid).  It counts the slots of every expert before
 // its own and in all (from the slots, or from the counting kernel's table plus the part of its own
 // chunk), ranks its slots in order, and copies each of its tokens' rows to the token's up to top_k
-// places, read once.  Padding rows and the row -> slot table's -1 entries are shared out evenly.
+// places, read once: a warp of its own ranks the next batch while the others copy.  Padding rows and the row -> slot table's -1 entries are shared out evenly.
+constexpr int kMoePermuteThreads = kMoeThreads + 32;
+
 template <int VB>
-__global__ void __launch_bounds__(kMoeThreads)
+__global__ void __launch_bounds__(kMoePermuteThreads)
 moe_permute_kernel(const PermuteArgs a) {
     using V = typename MoeVec<VB>::type;
-    constexpr int UN = 4;                                   // vectors per lane and unit of copying
+    // vectors per lane and unit of copying: 8 of 16 bytes (121 us against 125 with 4 at 8192 tokens x 8 slots x 8 KB)
+    constexpr int UN = VB == 16 ? 8 : 4;
     __shared__ int32_t before[kMoeMaxExperts];              // slots of the expert before the next one ranked
     __shared__ int32_t total[kMoeMaxExperts];
     __shared__ int32_t offs[kMoeMaxExperts + 1];
     __shared__ int32_t pads[kMoeMaxExperts + 1];
-    __shared__ int32_t place[kMoeBatchSlots];
+    __shared__ int32_t place[2][kMoeBatchSlots];
+    constexpr int NT = kMoePermuteThreads, CW = kMoeThreads / 32;   // threads; copying warps
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int E = a.E, k = a.top_k;
-    for (int e = tid; e < E; e += kMoeThreads) { before[e] = 0; total[e] = 0; }
+    for (int e = tid; e < E; e += NT) { before[e] = 0; total[e] = 0; }
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
@@ -131,17 +134,26 @@ moe_permute_kernel(const PermuteArgs a) {
     const int64_t start = (int64_t)t0 * k;
     if (a.counts == nullptr) {
         // total[] holds the slots from `start` on until the two are added below
-        for (int64_t i = tid; i < a.n; i += kMoeThreads) {
-            const int e = a.ids[i];
-            if (e >= 0 && e < E) atomicAdd(i < start ? &before[e] : &total[e], 1);
-            else if (e >= E && blockIdx.x == 0) atomicExch(&g_device_error, kErrBadSlot);
+        for (int64_t i0 = 0; i0 < a.n; i0 += 4 * NT) {
+            int e[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t i = i0 + q * NT + tid;
+                e[q] = i < a.n ? a.ids[i] : -1;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (e[q] >= 0 && e[q] < E) atomicAdd(i0 + q * NT + tid < start ? &before[e[q]] : &total[e[q]], 1);
+                else if (e[q] >= E && blockIdx.x == 0) atomicExch(&g_device_error, kErrBadSlot);
+            }
         }
         __syncthreads();
-        for (int e = tid; e < E; e += kMoeThreads) total[e] += before[e];
+        for (int e = tid; e < E; e += NT) total[e] += before[e];
     } else {
         const int own = (int)(start / a.chunk);             // chunks before this one lie before `start`
-        for (int e = tid; e < E; e += kMoeThreads) {
+        for (int e = tid; e < E; e += NT) {
             int32_t b = 0, all = 0;
+#pragma unroll 16
             for (int c = 0; c < kMoeCountChunks; ++c) {
                 const int32_t v = a.counts[(int64_t)c * E + e];
                 all += v;
@@ -151,7 +163,7 @@ moe_permute_kernel(const PermuteArgs a) {
             total[e] = all;
         }
         __syncthreads();
-        for (int64_t i = own * a.chunk + tid; i < start; i += kMoeThreads) {
+        for (int64_t i = own * a.chunk + tid; i < start; i += NT) {
             const int e = a.ids[i];
             if (e >= 0 && e < E) atomicAdd(&before[e], 1);
         }
@@ -159,52 +171,58 @@ moe_permute_kernel(const PermuteArgs a) {
     __syncthreads();
     moe_scan(total, E, a.align, offs, pads);
     if (blockIdx.x == 0)
-        for (int e = tid; e <= E; e += kMoeThreads) a.indptr[e] = offs[e];
+        for (int e = tid; e <= E; e += NT) a.indptr[e] = offs[e];
 
-    // ---- this CTA's tokens, some at a time: rank their slots, then copy their rows ----
+    // ---- this CTA's tokens, some at a time: rank their slots, copy their rows ----
     const int64_t nv = a.row_bytes / VB;
     const int segs = (int)((nv + 32 * UN - 1) / (32 * UN));
     const int batch = kMoeBatchSlots / k;
-    for (int tb = t0; tb < t1; tb += batch) {
-        const int nt = min(batch, t1 - tb);
-        if (warp == 0) {
-            for (int s = 0; s < nt * k; s += 32) {
-                const int64_t i = (int64_t)tb * k + s + lane;
-                const bool in = s + lane < nt * k;
-                int e = in ? a.ids[i] : -1;
-                if (e >= E) {
-                    if (a.counts != nullptr) atomicExch(&g_device_error, kErrBadSlot);
-                    e = -1;
-                }
-                const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-                int32_t row = -1;
-                if (e >= 0) row = offs[e] + before[e] + __popc(same & ((1u << lane) - 1u));
-                __syncwarp();
-                if (e >= 0 && lane == __ffs(same) - 1) before[e] += __popc(same);
-                __syncwarp();
-                if (in) {
-                    place[s + lane] = row;
-                    a.idx[i] = row;
-                    if (row >= 0) a.inv[row] = (int32_t)i;
-                }
+    auto rank = [&](int tb, int32_t* dst) {
+        const int ns = min(batch, t1 - tb) * k;
+        for (int s = 0; s < ns; s += 32) {
+            const int64_t i = (int64_t)tb * k + s + lane;
+            const bool in = s + lane < ns;
+            int e = in ? a.ids[i] : -1;
+            if (e >= E) {
+                if (a.counts != nullptr) atomicExch(&g_device_error, kErrBadSlot);
+                e = -1;
+            }
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+            int32_t row = -1;
+            if (e >= 0) row = offs[e] + before[e] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e >= 0 && lane == __ffs(same) - 1) before[e] += __popc(same);
+            __syncwarp();
+            if (in) {
+                dst[s + lane] = row;
+                a.idx[i] = row;
+                if (row >= 0) a.inv[row] = (int32_t)i;
             }
         }
-        __syncthreads();
-        for (int u = warp; u < nt * segs; u += kMoeThreads / 32) {
-            const int t = u / segs, sg = u % segs;
-            const V* src = reinterpret_cast<const V*>(a.x + (int64_t)(tb + t) * a.row_bytes) + (int64_t)sg * 32 * UN;
-            const int64_t left = nv - (int64_t)sg * 32 * UN;
-            V v[UN];
-#pragma unroll
-            for (int q = 0; q < UN; ++q)
-                if (q * 32 + lane < left) v[q] = src[q * 32 + lane];
-            for (int j = 0; j < k; ++j) {
-                const int32_t row = place[t * k + j];
-                if (row < 0) continue;
-                V* dst = reinterpret_cast<V*>(a.rows + (int64_t)row * a.row_bytes) + (int64_t)sg * 32 * UN;
+    };
+    if (warp == CW && t0 < t1) rank(t0, place[0]);
+    __syncthreads();
+    for (int tb = t0, cur = 0; tb < t1; tb += batch, cur ^= 1) {
+        if (warp == CW) {
+            if (tb + batch < t1) rank(tb + batch, place[cur ^ 1]);
+        } else {
+            const int nt = min(batch, t1 - tb);
+            for (int u = warp; u < nt * segs; u += CW) {
+                const int t = u / segs, sg = u % segs;
+                const V* src = reinterpret_cast<const V*>(a.x + (int64_t)(tb + t) * a.row_bytes) + (int64_t)sg * 32 * UN;
+                const int64_t left = nv - (int64_t)sg * 32 * UN;
+                V v[UN];
 #pragma unroll
                 for (int q = 0; q < UN; ++q)
-                    if (q * 32 + lane < left) dst[q * 32 + lane] = v[q];
+                    if (q * 32 + lane < left) v[q] = src[q * 32 + lane];
+                for (int j = 0; j < k; ++j) {
+                    const int32_t row = place[cur][t * k + j];
+                    if (row < 0) continue;
+                    V* dst = reinterpret_cast<V*>(a.rows + (int64_t)row * a.row_bytes) + (int64_t)sg * 32 * UN;
+#pragma unroll
+                    for (int q = 0; q < UN; ++q)
+                        if (q * 32 + lane < left) dst[q * 32 + lane] = v[q];
+                }
             }
         }
         __syncthreads();
@@ -212,7 +230,7 @@ moe_permute_kernel(const PermuteArgs a) {
 
     // ---- padding rows, and the -1 entries of the row -> slot table ----
     const int npad = pads[E];
-    const int gw = blockIdx.x * (kMoeThreads / 32) + warp, nw = gridDim.x * (kMoeThreads / 32);
+    const int gw = blockIdx.x * (NT / 32) + warp, nw = gridDim.x * (NT / 32);
     for (int p = gw; p < npad; p += nw) {
         int lo = 0, hi = E - 1;                             // the last expert with pads[e] <= p
         while (lo < hi) {
@@ -226,7 +244,7 @@ moe_permute_kernel(const PermuteArgs a) {
             for (int64_t q = lane; q < nv; q += 32) dst[q] = V{};
         }
     }
-    for (int64_t r = (int64_t)offs[E] + blockIdx.x * kMoeThreads + tid; r < a.capacity; r += gridDim.x * kMoeThreads)
+    for (int64_t r = (int64_t)offs[E] + blockIdx.x * NT + tid; r < a.capacity; r += gridDim.x * NT)
         a.inv[r] = -1;
 }
 
@@ -236,38 +254,91 @@ moe_permute_kernel(const PermuteArgs a) {
 
 enum class MoeType { BF16, FP16, FP32 };
 
-// VE elements of one type: loaded together, as fp32, and rounded back (nearest, ties to even).
-template <MoeType TY, int VE>
-struct MoePack {
-    static constexpr int ES = TY == MoeType::FP32 ? 4 : 2;
-    using V = typename MoeVec<ES * VE>::type;
-    static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VE]) {
-        unpack(reinterpret_cast<const V*>(p)[i], f);
+template <MoeType TY> struct MoeElem { using type = uint16_t; };
+template <> struct MoeElem<MoeType::FP32> { using type = float; };
+
+template <MoeType TY>
+__device__ __forceinline__ float to_f32(typename MoeElem<TY>::type h) {
+    if constexpr (TY == MoeType::FP32) return h;
+    else if constexpr (TY == MoeType::BF16) return __uint_as_float((uint32_t)h << 16);
+    else return __half2float(__ushort_as_half(h));
+}
+
+template <MoeType TY>
+__device__ __forceinline__ typename MoeElem<TY>::type from_f32(float f) {   // nearest, ties to even
+    if constexpr (TY == MoeType::FP32) return f;
+    else if constexpr (TY == MoeType::BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+    else return __half_as_ushort(__float2half_rn(f));
+}
+
+// A warp's share of a row: 256 elements from element e0 on, eight per lane.  VEC: the lane's eight are
+// neighbours, one 16-byte access (two for fp32); the row length is a multiple of 8 and rows start on
+// 16-byte boundaries.  Otherwise they are 32 apart, so that any alignment is read and written in
+// coalesced element accesses.
+template <MoeType TY, bool VEC>
+struct RowChunk {
+    using E = typename MoeElem<TY>::type;
+    static constexpr int NW = 8 * (int)sizeof(E) / 16;
+    union Raw {
+        uint4 w[NW];
+        E e[8];
+    };
+    static __device__ __forceinline__ int64_t at(int64_t e0, int lane, int i) {
+        return VEC ? e0 + lane * 8 + i : e0 + i * 32 + lane;
     }
-    static __device__ __forceinline__ void unpack(const V& v, float (&f)[VE]) {
-        if constexpr (TY == MoeType::FP32) {
-            memcpy(f, &v, sizeof(v));
-        } else {
-            uint16_t h[VE];
-            memcpy(h, &v, sizeof(v));
+    static __device__ __forceinline__ Raw load(const void* row, int64_t e0, int64_t H, int lane) {
+        Raw r;
+        const E* p = static_cast<const E*>(row);
+        if constexpr (VEC) {
+            if (at(e0, lane, 0) < H) {
 #pragma unroll
-            for (int q = 0; q < VE; ++q)
-                f[q] = TY == MoeType::BF16 ? __uint_as_float((uint32_t)h[q] << 16) : __half2float(__ushort_as_half(h[q]));
+                for (int i = 0; i < NW; ++i) r.w[i] = reinterpret_cast<const uint4*>(p + at(e0, lane, 0))[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.e[i] = at(e0, lane, i) < H ? p[at(e0, lane, i)] : E(0);
+        }
+        return r;
+    }
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
+        if constexpr (TY == MoeType::FP32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = r.e[i];
+        } else {
+            const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = to_f32<TY>((uint16_t)(u[i] & 0xFFFFu));
+                f[2 * i + 1] = to_f32<TY>((uint16_t)(u[i] >> 16));
+            }
         }
     }
-    static __device__ __forceinline__ V pack(const float (&f)[VE]) {
-        V v;
+    static __device__ __forceinline__ void store(void* row, int64_t e0, int64_t H, int lane, const float (&f)[8]) {
+        E* p = static_cast<E*>(row);
+        Raw r;
         if constexpr (TY == MoeType::FP32) {
-            memcpy(&v, f, sizeof(v));
-        } else {
-            uint16_t h[VE];
 #pragma unroll
-            for (int q = 0; q < VE; ++q)
-                h[q] = TY == MoeType::BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[q]))
-                                           : __half_as_ushort(__float2half_rn(f[q]));
-            memcpy(&v, h, sizeof(v));
+            for (int i = 0; i < 8; ++i) r.e[i] = f[i];
+        } else {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = (uint32_t)from_f32<TY>(f[2 * i]) | ((uint32_t)from_f32<TY>(f[2 * i + 1]) << 16);
+            r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        return v;
+        if constexpr (VEC) {
+            if (at(e0, lane, 0) < H) {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) reinterpret_cast<uint4*>(p + at(e0, lane, 0))[i] = r.w[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (at(e0, lane, i) < H) p[at(e0, lane, i)] = r.e[i];
+        }
     }
 };
 
@@ -276,25 +347,34 @@ struct UnpermuteArgs {
     const int32_t* idx;      // [T, top_k]: slot -> row
     const float* w;          // [T, top_k] or null (all 1)
     void* out;               // [T, H]
-    int64_t nv;              // vectors per row
+    int64_t H;
     int64_t units;           // T * segs
-    int top_k, rows, segs;
+    int top_k, rows, segs;   // segs = ceil(H / 256)
 };
 
-// A warp per (token, 32 vectors of the row): the loads of four slots are issued before the first
-// multiply.
-template <MoeType TY, int VE>
+template <MoeType TY>
+__device__ __forceinline__ const void* row_at(const void* base, int64_t row, int64_t H) {
+    return static_cast<const typename MoeElem<TY>::type*>(base) + row * H;
+}
+
+template <MoeType TY>
+__device__ __forceinline__ void* row_at(void* base, int64_t row, int64_t H) {
+    return static_cast<typename MoeElem<TY>::type*>(base) + row * H;
+}
+
+// A warp per (token, 256 elements of the row): the loads of four slots (two of fp32) are issued before the
+// first multiply.
+template <MoeType TY, bool VEC>
 __global__ void __launch_bounds__(kMoeThreads)
 moe_unpermute_kernel(const UnpermuteArgs a) {
-    using P = MoePack<TY, VE>;
-    using V = typename P::V;
+    using C = RowChunk<TY, VEC>;
+    constexpr int JC = TY == MoeType::FP32 ? 2 : 4;
     const int lane = threadIdx.x & 31;
     const int64_t u = (int64_t)blockIdx.x * (kMoeThreads / 32) + (threadIdx.x >> 5);
     grid_dependency_wait();
     grid_launch_dependents();
     if (u >= a.units) return;
-    const int64_t t = u / a.segs;
-    const int sg = (int)(u % a.segs);
+    const int64_t t = u / a.segs, e0 = (u - t * a.segs) * 256;
     const int k = a.top_k;
     int32_t my_row = -1;
     float my_w = 1.0f;
@@ -306,32 +386,30 @@ moe_unpermute_kernel(const UnpermuteArgs a) {
             my_row = -1;
         }
     }
-    const int64_t c = (int64_t)sg * 32 + lane;
-    const bool on = c < a.nv;
-    float acc[VE];
+    float acc[8];
 #pragma unroll
-    for (int q = 0; q < VE; ++q) acc[q] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += 4) {
-        V v[4];
-        int32_t r[4];
-        float w[4];
+    for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += JC) {
+        typename C::Raw v[JC];
+        int32_t r[JC];
+        float w[JC];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {                       // lanes past top_k hold row -1 (j0 + j < 32)
+        for (int j = 0; j < JC; ++j) {                      // lanes past top_k hold row -1 (j0 + j < 32)
             r[j] = __shfl_sync(0xFFFFFFFFu, my_row, j0 + j);
             w[j] = __shfl_sync(0xFFFFFFFFu, my_w, j0 + j);
-            if (r[j] >= 0 && on) v[j] = __ldg(reinterpret_cast<const V*>(a.y) + (int64_t)r[j] * a.nv + c);
+            if (r[j] >= 0) v[j] = C::load(row_at<TY>(a.y, r[j], a.H), e0, a.H, lane);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (r[j] >= 0 && on) {
-                float f[VE];
-                P::unpack(v[j], f);
+        for (int j = 0; j < JC; ++j) {
+            if (r[j] >= 0) {
+                float f[8];
+                C::unpack(v[j], f);
 #pragma unroll
-                for (int q = 0; q < VE; ++q) acc[q] = a.w != nullptr ? fmaf(w[j], f[q], acc[q]) : acc[q] + f[q];
+                for (int q = 0; q < 8; ++q) acc[q] = a.w != nullptr ? fmaf(w[j], f[q], acc[q]) : acc[q] + f[q];
             }
         }
     }
-    if (on) reinterpret_cast<V*>(a.out)[t * a.nv + c] = P::pack(acc);
+    C::store(row_at<TY>(a.out, t, a.H), e0, a.H, lane, acc);
 }
 
 struct UnpermuteBwdArgs {
@@ -343,45 +421,50 @@ struct UnpermuteBwdArgs {
     const float* w;          // [T, top_k] or null
     void* gy;                // [rows, H]
     float* gw;               // [T, top_k] or null
-    int64_t nv;
+    int64_t H;
     int T, top_k, rows;
 };
 
-// A CTA per token: g[t] is read once per four slots (from L1 after the first), each slot's row of y
-// once; gy's rows are written and the four dot products kept per thread, then summed over the CTA
-// in a fixed order.  The CTAs past T write zeros into the padding rows of the segments.
-template <MoeType TY, int VE>
-__global__ void __launch_bounds__(kMoeThreads)
+// A CTA per token: g[t] is read once per two slots (from L1 after the first), each slot's row of y once; gy's
+// rows are written and the two dot products kept per thread, then summed over the CTA in a fixed order.  The
+// CTAs past T write zeros into the padding rows of the segments.  128 threads and two slots at a time: 109 us at
+// 4096 tokens x 8 slots x 8 KB (5.3 TB/s); 256 threads and four slots 114, eight slots 128 (fewer CTAs resident).
+constexpr int kMoeBwdThreads = 128;
+constexpr int kMoeBwdSlots = 2;
+
+template <MoeType TY, bool VEC>
+__global__ void __launch_bounds__(kMoeBwdThreads)
 moe_unpermute_bwd_kernel(const UnpermuteBwdArgs a) {
-    using P = MoePack<TY, VE>;
-    using V = typename P::V;
-    __shared__ float part[4][kMoeThreads / 32];
+    using C = RowChunk<TY, VEC>;
+    constexpr int JC = kMoeBwdSlots;
+    __shared__ float part[JC][kMoeBwdThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
     if (blockIdx.x >= a.T) {
         const int used = min(*a.total, a.rows);
         const int64_t step = (int64_t)(gridDim.x - a.T) * nw * 32;
+        const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         for (int64_t r0 = ((int64_t)(blockIdx.x - a.T) * nw + warp) * 32; r0 < used; r0 += step) {
             const bool pad = r0 + lane < used && a.inv[r0 + lane] < 0;
             uint32_t m = __ballot_sync(0xFFFFFFFFu, pad);
             while (m) {
-                const int64_t r = r0 + __ffs(m) - 1;
+                void* row = row_at<TY>(a.gy, r0 + __ffs(m) - 1, a.H);
                 m &= m - 1;
-                V* dst = reinterpret_cast<V*>(a.gy) + r * a.nv;
-                for (int64_t q = lane; q < a.nv; q += 32) dst[q] = V{};
+                for (int64_t e0 = 0; e0 < a.H; e0 += 256) C::store(row, e0, a.H, lane, zero);
             }
         }
         return;
     }
     const int64_t t = blockIdx.x;
     const int k = a.top_k;
-    const V* g = reinterpret_cast<const V*>(a.g) + t * a.nv;
-    for (int j0 = 0; j0 < k; j0 += 4) {
-        int32_t r[4];
-        float w[4], dot[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const void* g = row_at<TY>(a.g, t, a.H);
+    for (int j0 = 0; j0 < k; j0 += JC) {
+        int32_t r[JC];
+        float w[JC], dot[JC];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < JC; ++j) {
+            dot[j] = 0.0f;
             r[j] = j0 + j < k ? a.idx[t * k + j0 + j] : -1;
             w[j] = j0 + j < k && a.w != nullptr ? a.w[t * k + j0 + j] : 1.0f;
             if (r[j] >= a.rows) {
@@ -389,38 +472,38 @@ moe_unpermute_bwd_kernel(const UnpermuteBwdArgs a) {
                 r[j] = -1;
             }
         }
-        for (int64_t c = tid; c < a.nv; c += blockDim.x) {
-            const V gv = g[c];
-            V yv[4];
+        for (int64_t e0 = (int64_t)warp * 256; e0 < a.H; e0 += nw * 256) {
+            const typename C::Raw gv = C::load(g, e0, a.H, lane);
+            typename C::Raw yv[JC];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r[j] >= 0 && a.gw != nullptr) yv[j] = __ldg(reinterpret_cast<const V*>(a.y) + (int64_t)r[j] * a.nv + c);
-            float gf[VE];
-            P::unpack(gv, gf);
+            for (int j = 0; j < JC; ++j)
+                if (r[j] >= 0 && a.gw != nullptr) yv[j] = C::load(row_at<TY>(a.y, r[j], a.H), e0, a.H, lane);
+            float gf[8];
+            C::unpack(gv, gf);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < JC; ++j) {
                 if (r[j] < 0) continue;
-                float o[VE];
+                float o[8];
                 if (a.gw != nullptr) {
-                    float yf[VE];
-                    P::unpack(yv[j], yf);
+                    float yf[8];
+                    C::unpack(yv[j], yf);
 #pragma unroll
-                    for (int q = 0; q < VE; ++q) dot[j] = fmaf(gf[q], yf[q], dot[j]);
+                    for (int q = 0; q < 8; ++q) dot[j] = fmaf(gf[q], yf[q], dot[j]);
                 }
 #pragma unroll
-                for (int q = 0; q < VE; ++q) o[q] = w[j] * gf[q];
-                reinterpret_cast<V*>(a.gy)[(int64_t)r[j] * a.nv + c] = P::pack(o);
+                for (int q = 0; q < 8; ++q) o[q] = w[j] * gf[q];
+                C::store(row_at<TY>(a.gy, r[j], a.H), e0, a.H, lane, o);
             }
         }
         if (a.gw != nullptr) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < JC; ++j) {
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
                 if (lane == 0) part[j][warp] = dot[j];
             }
             __syncthreads();
-            if (tid < 4 && j0 + tid < k) {
+            if (tid < JC && j0 + tid < k) {
                 float s = part[tid][0];
                 for (int q = 1; q < nw; ++q) s += part[tid][q];
                 a.gw[t * k + j0 + tid] = s;                 // an inactive slot's sums are all 0

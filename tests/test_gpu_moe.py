@@ -42,8 +42,9 @@ SHAPES = [
     (64, 2, 8, 4096, BF, 128, 0.0, "mixed"),        # the decode batch
     (20, 4, 16, 40, BF, 128, 1.0, "mixed"),         # no active slot
     (300, 8, 64, 136, FP, 3, 0.0, "one"),           # one expert holds all
-    (2048, 8, 96, 72, BF, 128, 0.05, "mixed"),      # 16384 slots: the largest self-counted
-    (2049, 8, 96, 72, BF, 128, 0.05, "mixed"),      # one more: the counting kernel
+    (512, 8, 96, 72, BF, 128, 0.05, "mixed"),       # 4096 slots: the most that each CTA counts itself
+    (513, 8, 96, 72, BF, 128, 0.05, "mixed"),       # one token more: the counting kernel
+    (2049, 8, 96, 2056, BF, 128, 0.05, "mixed"),
     (9001, 5, 1024, 16, HF, 16, 0.05, "mixed"),
     (30000, 1, 3, 8, BF, 128, 0.0, "mixed"),
     (4000, 8, 2, 16, BF, 128, 0.0, "one"),
