@@ -1426,13 +1426,12 @@ nvfp4lora_status nvfp4lora_fp8_quantize(const void* x, int64_t rows, int64_t H, 
     const bool vec = H % 8 == 0 && aligned(x, 16) && aligned(q, 8);
     return by_type(dtype, [&](auto ty) {
         constexpr MoeType TY = decltype(ty)::value;
+        const int64_t tiles = (rows + 127) / 128 * groups;
         if (block_rows == 128)
-            return vec ? launch_dependent("quantize launch", quantize_fp8_blocks_kernel<TY>, brows * groups, 256, s, a)
-                       : launch_dependent("quantize launch", blocks_fp8_kernel<TY>, brows * groups, 256, s, a);
-        if (!vec) return launch_dependent("quantize launch", row_fp8_kernel<TY, false>, rows, 256, s, a);
-        const int64_t want = (rows * groups + 15) / 16;
-        return launch_dependent("quantize launch", quantize_fp8_rows_kernel<TY>,
-                                std::min<int64_t>(want, (int64_t)info->sms * 8), 256, s, a);
+            return vec ? launch_dependent("quantize launch", quantize_fp8_tile_kernel<TY, true>, tiles, 256, s, a)
+                       : launch_dependent("quantize launch", blocks_fp8_kernel<TY>, tiles, 256, s, a);
+        return vec ? launch_dependent("quantize launch", quantize_fp8_tile_kernel<TY, false>, tiles, 256, s, a)
+                   : launch_dependent("quantize launch", row_fp8_kernel<TY, false>, rows, 256, s, a);
     });
 }
 
@@ -1472,13 +1471,28 @@ nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(const void* x, void* residual, c
         constexpr MoeType TY = decltype(ty)::value;
         // longer rows than the registers of a CTA hold are read twice
         if (H > kNormMaxThreads * 8 * 4) return launch_dependent("norm launch", row_fp8_kernel<TY, true>, rows, 256, s, a);
-        auto go = [&](auto kernel, int per) {
-            return launch_dependent("norm launch", kernel, rows, (int)((H + 256 * per - 1) / (256 * per) * 32), s, a);
-        };
-        if (H <= 2048) return vec ? go(rmsnorm_fp8_kernel<TY, 1, true>, 1) : go(rmsnorm_fp8_kernel<TY, 1, false>, 1);
-        if (H <= kNormMaxThreads * 8 * 2)
-            return vec ? go(rmsnorm_fp8_kernel<TY, 2, true>, 2) : go(rmsnorm_fp8_kernel<TY, 2, false>, 2);
-        return vec ? go(rmsnorm_fp8_kernel<TY, 4, true>, 4) : go(rmsnorm_fp8_kernel<TY, 4, false>, 4);
+        // Chunks per warp: few where there are few rows, so that a row's latency is spread over many warps (16 x
+        // 4096: 1.96 us with one, 2.3 with two), and for short rows (4096 x 4096: 20.1 us with two, 22.7 with four);
+        // four for long ones, so that more rows are in flight per SM (8192 x 8192: 77 us with four, 87 with two).
+        // Four chunks of element accesses do not fit the registers of two CTAs.
+        const bool few = rows < 8 * (int64_t)info->sms;
+        if (H <= 512 && !few) {
+            // a warp per row: 65536 x 512 43 us, 68 with a CTA of two warps per row
+            const int64_t grid = (rows + kNormShortRows - 1) / kNormShortRows;
+            if (H <= 256)
+                return vec ? launch_dependent("norm launch", rmsnorm_fp8_kernel<TY, 1, true, true>, grid, 32 * kNormShortRows, s, a)
+                           : launch_dependent("norm launch", rmsnorm_fp8_kernel<TY, 1, false, true>, grid, 32 * kNormShortRows, s, a);
+            return vec ? launch_dependent("norm launch", rmsnorm_fp8_kernel<TY, 2, true, true>, grid, 32 * kNormShortRows, s, a)
+                       : launch_dependent("norm launch", rmsnorm_fp8_kernel<TY, 2, false, true>, grid, 32 * kNormShortRows, s, a);
+        }
+        const int64_t one = few ? kNormMaxThreads * 8 : 2048;
+        const int64_t two = few || !vec ? kNormMaxThreads * 16 : 4096;
+        const int per = H <= one ? 1 : H <= two ? 2 : 4;
+        const int threads = (int)((H + 256 * per - 1) / (256 * per)) * 32;
+        auto go = [&](auto kernel) { return launch_dependent("norm launch", kernel, rows, threads, s, a); };
+        if (per == 1) return vec ? go(rmsnorm_fp8_kernel<TY, 1, true, false>) : go(rmsnorm_fp8_kernel<TY, 1, false, false>);
+        if (per == 2) return vec ? go(rmsnorm_fp8_kernel<TY, 2, true, false>) : go(rmsnorm_fp8_kernel<TY, 2, false, false>);
+        return vec ? go(rmsnorm_fp8_kernel<TY, 4, true, false>) : go(rmsnorm_fp8_kernel<TY, 4, false, false>);
     });
 }
 

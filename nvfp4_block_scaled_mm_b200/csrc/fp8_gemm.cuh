@@ -6,6 +6,9 @@
 // (powers of two, or e4m3): each P_kb is formed in TMEM by itself, read back and added to an fp32
 // accumulator in registers, acc = fma(sa * sb, P_kb, acc).
 //
+// Scales and bias are read with plain loads after the dependency wait: read-only (nc) loads carry no ordering
+// against it, and the compiler moved them ahead of it, where the kernel before was still writing them.
+//
 // A cluster of two CTAs computes one 256 x 256 output tile per step with tcgen05.mma.cta_group::2
 // (kind::f8f6f4, M = 256, N = 256, K = 32): each CTA loads its own 128 rows of A and 128 of the
 // tile's 256 B rows, 32 KB per CTA and K block.  The TMEM holds two 256-column accumulators used
@@ -323,13 +326,13 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
             for (int k = 0; k < 128; ++k) acc[k] = 0.0f;
             // the scales of the next block, loaded one block ahead; they are multiplied when used (a multiply
             // here would stall the warp on the loads)
-            float sa_next = __ldg(sa), sb_next = __ldg(sb);
+            float sa_next = *sa, sb_next = *sb;
             for (int kb = 0; kb < args.kblocks; ++kb, ++g) {
                 const uint32_t buf = g & 1;
                 const uint64_t ss = dup2(sa_next * sb_next);
                 if (kb + 1 < args.kblocks) {
-                    sa_next = __ldg(sa + (kb + 1) * args.stride_ak);
-                    sb_next = __ldg(sb + kb + 1);
+                    sa_next = sa[(kb + 1) * args.stride_ak];
+                    sb_next = sb[kb + 1];
                 }
                 if (!__all_sync(kAll, mbar_wait_short(&acc_full[buf], (g >> 1) & 1, abort_flag))) { ok = false; break; }
                 tc_fence_after();
@@ -360,7 +363,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                 if (args.bias != nullptr) {
 #pragma unroll
                     for (int k = 0; k < COLS; ++k)
-                        acc[x + k] = __fadd_rn(acc[x + k], __uint_as_float((uint32_t)__ldg(args.bias + min(col0 + x + k, args.N - 1)) << 16));
+                        acc[x + k] = __fadd_rn(acc[x + k], __uint_as_float((uint32_t)args.bias[min(col0 + x + k, args.N - 1)] << 16));
                 }
                 if (args.vec_out && lane == 0) bulk_wait_group_read<0>();   // its previous store has read the box
                 __syncwarp();

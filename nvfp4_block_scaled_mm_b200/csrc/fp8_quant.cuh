@@ -77,20 +77,28 @@ __device__ __forceinline__ float cta_sum(float s, float* red) {
     return t;
 }
 
-// ---- norm: a CTA per row, the row kept in registers (NV chunks of 256 elements per warp) ----
+// ---- norm: the row kept in registers (NV chunks of 256 elements per warp); a CTA per row, or, with SHORT, a warp
+// per row of up to 1024 elements ----
 // HBM-bound: 2 + 1 bytes per element (16-bit types), and 4 more with a residual.  A chunk is two 1 x 128
 // groups: with VEC (aligned rows, H % 8 == 0) one per half-warp, otherwise the lanes' first and last four.
-template <MoeType TY, int NV, bool VEC>
-__global__ void __launch_bounds__(kNormMaxThreads)
+constexpr int kNormShortRows = 8;          // rows (warps) of a SHORT CTA
+
+template <MoeType TY, int NV, bool VEC, bool SHORT>
+__global__ void __launch_bounds__(kNormMaxThreads, NV == 4 && VEC && !SHORT ? 2 : 0)
 rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
     using C = RowChunk<TY, VEC>;
     __shared__ float red[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int64_t row = blockIdx.x, H = a.H;
+    const int lane = threadIdx.x & 31, warp = SHORT ? 0 : threadIdx.x >> 5, nw = SHORT ? 1 : blockDim.x >> 5;
+    const int64_t row = SHORT ? (int64_t)blockIdx.x * kNormShortRows + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    const int64_t H = a.H;
+    if (SHORT && row >= a.rows) return;        // no barrier follows
     const void* x = row_at<TY>(a.x, row, H);
     void* res = a.residual != nullptr ? row_at<TY>(a.residual, row, H) : nullptr;
     float h[NV][8];
-    typename C::Raw wt[NV];
+    // rows of four chunks per warp load the weight after the sum: held across it, it would spill at the 64
+    // registers of two CTAs of 512 threads
+    constexpr bool kLate = NV == 4;
+    typename C::Raw wt[kLate ? 1 : NV];
     grid_dependency_wait();
     grid_launch_dependents();
     float ss = 0.0f;
@@ -101,7 +109,7 @@ rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
             const int64_t e0 = (int64_t)(warp + i * nw) * 256;
             xr[i] = C::load(x, e0, H, lane);
             if (res != nullptr) rr[i] = C::load(res, e0, H, lane);
-            wt[i] = C::load(a.weight, e0, H, lane);
+            if constexpr (!kLate) wt[i] = C::load(a.weight, e0, H, lane);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -117,12 +125,19 @@ rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
             for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);   // elements past H are 0
         }
     }
-    const float rms = rsqrtf(cta_sum(ss, red) / (float)H + a.eps);
+    if constexpr (SHORT) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+    } else {
+        ss = cta_sum(ss, red);
+    }
+    const float rms = rsqrtf(ss / (float)H + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t e0 = (int64_t)(warp + i * nw) * 256;
         float y[8];
-        C::unpack(wt[i], y);
+        if constexpr (!kLate) C::unpack(wt[i], y);
+        else C::unpack(C::load(a.weight, e0, H, lane), y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rms * y[e];
         float* sc = a.scales + row * a.stride_r;
@@ -210,57 +225,13 @@ row_fp8_kernel(const Fp8QuantArgs a) {
     }
 }
 
-// ---- quantizer, 1 x 128 groups: half a warp per group, four groups' loads in flight per lane ----
-// HBM-bound: 2 bytes read (16-bit types) and 1 written per element.  H % 8 == 0, aligned rows.
-template <MoeType TY>
+// ---- quantizer of aligned rows (H % 8 == 0): a CTA per 128 rows x 128 columns, kept in registers ----
+// HBM-bound: 2 bytes read (16-bit types) and 1 written per element.  Sixteen lanes hold 128 columns of a row, each
+// thread 8 rows of 8 columns, all loaded before the first is used.  BLOCK: one scale for the tile (28672 x 8192 bf16:
+// 102 us, 6.9 TB/s), otherwise one per row.
+template <MoeType TY, bool BLOCK>
 __global__ void __launch_bounds__(256)
-quantize_fp8_rows_kernel(const Fp8QuantArgs a) {
-    using R = RowChunk<TY, true>;
-    constexpr int UN = TY == MoeType::FP32 ? 2 : 4;
-    const int64_t groups = (a.H + 127) / 128;
-    const int nv = (int)(a.H / 8);
-    const int hl = threadIdx.x & 15;
-    const int64_t total = a.rows * groups;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    // half-warp hw of the grid takes the groups hw, hw + step, ...; a warp's lanes stay together
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x / 16);
-    const int64_t first = (int64_t)blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4);
-    for (int64_t g0 = first; g0 - (first & 1) < total; g0 += step * UN) {
-        typename R::Raw raw[UN];
-        int64_t row[UN];
-        int gr[UN];
-        bool on[UN];
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int64_t g = g0 + u * step;
-            row[u] = g / groups;
-            gr[u] = (int)(g - row[u] * groups);
-            on[u] = g < total && gr[u] * 16 + hl < nv;
-            if (on[u]) raw[u] = R::load(a.x, (row[u] * nv + gr[u] * 16 + hl) * 8, INT64_MAX, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-            if (on[u]) R::unpack(raw[u], y);
-            float m = abs_max8(y);
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            m = fmaxf(m, kFp8Tiny);
-            if (on[u]) {
-                reinterpret_cast<uint2*>(a.q)[row[u] * nv + gr[u] * 16 + hl] = e4m3x8_scaled(y, __fdiv_rn(kFp8Max, m));
-                if (hl == 0) a.scales[row[u] * a.stride_r + gr[u] * a.stride_g] = __fdiv_rn(m, kFp8Max);
-            }
-        }
-    }
-}
-
-// ---- quantizer, 128 x 128 blocks: a CTA per block, the block kept in registers ----
-template <MoeType TY>
-__global__ void __launch_bounds__(256)
-quantize_fp8_blocks_kernel(const Fp8QuantArgs a) {
+quantize_fp8_tile_kernel(const Fp8QuantArgs a) {
     using R = RowChunk<TY, true>;
     __shared__ float red[8];
     const int nv = (int)(a.H / 8);
@@ -274,30 +245,43 @@ quantize_fp8_blocks_kernel(const Fp8QuantArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (c < nv && r0 + i * 16 < a.rows) raw[i] = R::load(a.x, ((r0 + i * 16) * nv + c) * 8, INT64_MAX, 0);
-    float m = 0.0f;
+    float inv = 0.0f;
+    if constexpr (BLOCK) {
+        float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c < nv && r0 + i * 16 < a.rows) {
-            float y[8];
-            R::unpack(raw[i], y);
-            m = fmaxf(m, abs_max8(y));
+        for (int i = 0; i < 8; ++i)
+            if (c < nv && r0 + i * 16 < a.rows) {
+                float y[8];
+                R::unpack(raw[i], y);
+                m = fmaxf(m, abs_max8(y));
+            }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+        __syncthreads();
+        m = kFp8Tiny;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+        inv = __fdiv_rn(kFp8Max, m);
+        if (threadIdx.x == 0) a.scales[br * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool on = c < nv && r0 + i * 16 < a.rows;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+        if (on) R::unpack(raw[i], y);
+        if constexpr (!BLOCK) {
+            float m = abs_max8(y);
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            m = fmaxf(m, kFp8Tiny);
+            inv = __fdiv_rn(kFp8Max, m);
+            if (on && (threadIdx.x & 15) == 0) a.scales[(r0 + i * 16) * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);
         }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = kFp8Tiny;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
-    const float inv = __fdiv_rn(kFp8Max, m);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c < nv && r0 + i * 16 < a.rows) {
-            float y[8];
-            R::unpack(raw[i], y);
-            reinterpret_cast<uint2*>(a.q)[(r0 + i * 16) * nv + c] = e4m3x8_scaled(y, inv);
-        }
-    if (threadIdx.x == 0) a.scales[br * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);
+        if (on) reinterpret_cast<uint2*>(a.q)[(r0 + i * 16) * nv + c] = e4m3x8_scaled(y, inv);
+    }
 }
 
 // ---- 128 x 128 blocks of any row length and alignment: a CTA per block, read twice ----

@@ -230,8 +230,8 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             for (int v = 0; v < PER; ++v) {
                 const int idx = v * ET + et, m = m0 + idx % MT, kb = kc + idx / MT;
                 const bool in = m < args.M && kb < k1;
-                pre_a[v] = in ? __ldg(args.a_scale + m * args.stride_am + kb * args.stride_ak) : 0.0f;
-                pre_b[v] = in ? __ldg(sb + kb) : 0.0f;
+                pre_a[v] = in ? args.a_scale[m * args.stride_am + kb * args.stride_ak] : 0.0f;
+                pre_b[v] = in ? sb[kb] : 0.0f;
             }
         };
         float acc[L::COLS];
@@ -297,7 +297,7 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             float* bv = reinterpret_cast<float*>(&bias);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (n0 + e < args.N) bv[e] = __uint_as_float((uint32_t)__ldg(args.bias + n0 + e) << 16);
+                if (n0 + e < args.N) bv[e] = __uint_as_float((uint32_t)args.bias[n0 + e] << 16);
         }
         for (int m = b0 + et / 32; m < b1; m += L::EW) {
             float4 v;

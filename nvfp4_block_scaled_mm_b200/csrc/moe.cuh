@@ -47,7 +47,7 @@ struct PermuteArgs {
 
 // Slots per expert of one chunk of the slots; a CTA per chunk.
 __global__ void __launch_bounds__(kMoeThreads)
-moe_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, int32_t* __restrict__ counts) {
+moe_count_kernel(const int32_t* ids, int64_t n, int64_t chunk, int E, int32_t* counts) {
     __shared__ int32_t hist[kMoeMaxExperts];
     for (int e = threadIdx.x; e < E; e += kMoeThreads) hist[e] = 0;
     __syncthreads();

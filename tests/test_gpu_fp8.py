@@ -247,7 +247,7 @@ def test_captured_layer_replays_on_new_inputs_and_a_side_stream():
     w = torch.ones(H, dtype=BF, device=DEV)
     w1, s1 = L.fp8_quantize(randn(F, H, dtype=BF, seed=1, std=0.1).to(DEV), block_rows=128)
     w2, s2 = L.fp8_quantize(randn(H, F, dtype=BF, seed=2, std=0.1).to(DEV), block_rows=128)
-    for T in (4, 300):
+    for T in (4, 24, 60, 100, 300, 700):
         x = randn(T, H, dtype=BF, seed=3).to(DEV)
         res = torch.zeros_like(x)
 
