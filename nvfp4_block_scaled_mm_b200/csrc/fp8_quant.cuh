@@ -245,7 +245,6 @@ quantize_fp8_tile_kernel(const Fp8QuantArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (c < nv && r0 + i * 16 < a.rows) raw[i] = R::load(a.x, ((r0 + i * 16) * nv + c) * 8, INT64_MAX, 0);
-    float inv = 0.0f;
     if constexpr (BLOCK) {
         float m = 0.0f;
 #pragma unroll
@@ -262,25 +261,42 @@ quantize_fp8_tile_kernel(const Fp8QuantArgs a) {
         m = kFp8Tiny;
 #pragma unroll
         for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
-        inv = __fdiv_rn(kFp8Max, m);
+        const float inv = __fdiv_rn(kFp8Max, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c < nv && r0 + i * 16 < a.rows) {
+                float y[8];
+                R::unpack(raw[i], y);
+                reinterpret_cast<uint2*>(a.q)[(r0 + i * 16) * nv + c] = e4m3x8_scaled(y, inv);
+            }
         if (threadIdx.x == 0) a.scales[br * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);
-    }
+    } else {
+        // lane i of the sixteen divides for row i, once for all of them
+        const int lane = threadIdx.x & 31, hl = threadIdx.x & 15;
+        float mine = 1.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool on = c < nv && r0 + i * 16 < a.rows;
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-        if (on) R::unpack(raw[i], y);
-        if constexpr (!BLOCK) {
-            float m = abs_max8(y);
+        for (int i = 0; i < 8; ++i) {
+            float m = 0.0f;
+            if (c < nv && r0 + i * 16 < a.rows) {
+                float y[8];
+                R::unpack(raw[i], y);
+                m = abs_max8(y);
+            }
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            m = fmaxf(m, kFp8Tiny);
-            inv = __fdiv_rn(kFp8Max, m);
-            if (on && (threadIdx.x & 15) == 0) a.scales[(r0 + i * 16) * a.stride_r + bc * a.stride_g] = __fdiv_rn(m, kFp8Max);
+            if (hl == i) mine = fmaxf(m, kFp8Tiny);
         }
-        if (on) reinterpret_cast<uint2*>(a.q)[(r0 + i * 16) * nv + c] = e4m3x8_scaled(y, inv);
+        const float inv_mine = __fdiv_rn(kFp8Max, mine);
+        if (hl < 8 && r0 + hl * 16 < a.rows) a.scales[(r0 + hl * 16) * a.stride_r + bc * a.stride_g] = __fdiv_rn(mine, kFp8Max);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float inv = __shfl_sync(0xFFFFFFFFu, inv_mine, (lane & 16) + i);
+            if (c < nv && r0 + i * 16 < a.rows) {
+                float y[8];
+                R::unpack(raw[i], y);
+                reinterpret_cast<uint2*>(a.q)[(r0 + i * 16) * nv + c] = e4m3x8_scaled(y, inv);
+            }
+        }
     }
 }
 
