@@ -253,12 +253,11 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
                 if (!ok) break;
                 tc_fence_after();
                 const float4* s4 = reinterpret_cast<const float4*>(cur + j * MT + cb);
-                constexpr int W = L::COLS < 32 || MT == 64 ? 16 : 32;   // columns per read
+                constexpr int W = 16;                  // columns per read
 #pragma unroll
                 for (int c = 0; c < L::COLS; c += W) {
                     uint32_t p[W];
-                    if constexpr (W == 32) tmem_load_32(tmem + lane_off + buf * MT + cb + c, p);
-                    else tmem_load_16(tmem + lane_off + buf * MT + cb + c, p);
+                    tmem_load_16(tmem + lane_off + buf * MT + cb + c, p);
                     tmem_load_wait();
                     if (c + W == L::COLS) {
                         tc_fence_before();

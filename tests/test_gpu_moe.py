@@ -354,3 +354,40 @@ def test_sorted_rows_through_the_grouped_product():
     size = want.abs().max().item()
     # each row is rounded to bf16 once by either product (their sums may differ in order), the total once more
     assert (out.cpu().double() - want).abs().max().item() <= 2.0 ** -7 * size + 2.0 ** -8 * size
+
+
+def test_sorted_rows_into_the_lora_delta_replayed():
+    """The rows and the table that one captured call writes are what the next reads, at every replay: sorted
+    tokens straight into the LoRA delta, against the same calls with the device idle in between."""
+    import nvfp4_block_scaled_mm_b200 as L
+    T, k, E, I, H, rank = 64, 2, 8, 512, 256, 16
+    a_banks = [rows_of(2 * rank, I, BF, 30 + e).to(DEV) for e in range(E)]
+    b_banks = [rows_of(2 * H, rank, BF, 50 + e).to(DEV) for e in range(E)]
+    wa, wb = L.fill_w_ptr(a_banks), L.fill_w_ptr(b_banks)
+    x, ids = rows_of(T, I, BF, 1).to(DEV), routing(T, k, E, 1).to(DEV)
+    w = torch.rand(T, k, device=DEV)
+    lids = (torch.arange(T, device=DEV) % 2).int()
+
+    def step(idle=lambda: None):
+        valid = ids.clamp(min=0)
+        out = torch.zeros(T, H, dtype=BF, device=DEV)
+        p = L.moe_permute(x, ids, E, align=8)
+        idle()
+        delta = L.bgmv_moe_gemm2_lora_delta(p.rows, p.expanded_idx_to_permuted_idx, wa, rank * I, wb, H * rank, valid, w,
+                                            lids, rank, H, out=out)
+        idle()
+        return delta, L.moe_unpermute(p.rows, p, w)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in range(2, 12):
+        x.copy_(rows_of(T, I, BF, seed))
+        ids.copy_(routing(T, k, E, seed))
+        want = step(torch.cuda.synchronize)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), seed
+    L.nvfp4lora_device_status()
