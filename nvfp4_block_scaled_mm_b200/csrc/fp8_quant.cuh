@@ -9,6 +9,10 @@
 // all in fp32: the sum of squares, y and the group maxima come from the unrounded h, so that q is
 // the only rounding to fewer bits on its path.
 // A NaN stays a NaN in q and is ignored by amax; an infinity makes its group's scale infinite.
+//
+// HBM-bound: the norm of 8192 x 8192 bf16 with residual and the normed rows kept runs 95 us (6.4 TB/s), of 65536 x 512
+// 37 us (6.4); the quantizer of 8192 x 8192 37 us by rows (5.5) and of 28672 x 8192 102 us by blocks (6.9, part of the
+// writes still in L2).  Sixteen rows take 2 us, launch latency.
 #pragma once
 
 #include <cstdint>
@@ -227,8 +231,8 @@ row_fp8_kernel(const Fp8QuantArgs a) {
 
 // ---- quantizer of aligned rows (H % 8 == 0): a CTA per 128 rows x 128 columns, kept in registers ----
 // HBM-bound: 2 bytes read (16-bit types) and 1 written per element.  Sixteen lanes hold 128 columns of a row, each
-// thread 8 rows of 8 columns, all loaded before the first is used.  BLOCK: one scale for the tile (28672 x 8192 bf16:
-// 102 us, 6.9 TB/s), otherwise one per row.
+// thread 8 rows of 8 columns, all loaded before the first is used.  BLOCK: one scale for the tile, otherwise one per
+// row.
 template <MoeType TY, bool BLOCK>
 __global__ void __launch_bounds__(256)
 quantize_fp8_tile_kernel(const Fp8QuantArgs a) {

@@ -13,6 +13,11 @@
 //     gy[row(t, j)] = w[t, j] * g[t],   gw[t, j] = <g[t], y[row(t, j)]>;
 // the gradient of the sorting is the sum without weights.  Sums are formed in fp32 in slot order
 // (gw: a fixed tree over the row) and rounded once.
+//
+// All of it is bound by HBM where there are many tokens (8 KB rows, 8 slots): sorting 8192 tokens 121 us
+// (5.4 TB/s; about 10 us of it are the two launches and the counting), its gradient 89 us (6.4 TB/s), the weighted sum
+// of 4096 tokens 47 us (6.1 TB/s) and its gradients 109 us (5.3 TB/s, half of it scattered writes).  A decode batch
+// takes 6 us (64 tokens, 768 rows written, 645 of them padding) and 1.7 us, launch latency.
 #pragma once
 
 #include <cstdint>
@@ -104,6 +109,8 @@ __device__ __forceinline__ void moe_scan(const int32_t* total, int E, int align,
     __syncthreads();
 }
 
+// One launch where every CTA can count all slots itself, two above kMoeSelfCountSlots (4096 slots 4.5 us; 16384
+// slots 17 us in one launch and 9 in two).
 // CTA c owns the tokens [T c / grid, T (c + 1) / grid).  It counts the slots of every expert before
 // its own and in all (from the slots, or from the counting kernel's table plus the part of its own
 // chunk), ranks its slots in order, and copies each of its tokens' rows to the token's up to top_k
