@@ -707,8 +707,9 @@ def _refuse_recording_in_capture(name: str, instead: str) -> None:
 
 class _MoePermuteFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, topk_ids, num_experts, align, zero_padding, out):
-        rows, m_indptr, idx, inv = _moe_permute(x, topk_ids, num_experts, align, zero_padding, out)
+    def forward(ctx, x, topk_ids, num_experts, align, zero_padding, capacity):
+        rows, m_indptr, idx, inv = _moe_permute(x, topk_ids, num_experts, align, zero_padding,
+                                                x.new_empty((capacity, x.shape[1])))
         ctx.save_for_backward(idx)
         ctx.mark_non_differentiable(m_indptr, idx, inv)
         return rows, m_indptr, idx, inv
@@ -729,8 +730,9 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
     inactive slot; an expert may occur twice).  Expert e's segment holds the rows of its slots in slot
     order (``t * top_k + j``) and is padded to a multiple of ``align`` rows (128 for the grouped
     call).  Padding rows are zeros, or left as they were with ``zero_padding=False``; rows from
-    ``m_indptr[E]`` on are left as they were.  ``out``: a ``[capacity, H]`` buffer for the rows with
-    ``capacity >= moe_capacity(T, top_k, E, align)``.  1 <= top_k <= 16, 1 <= E <= 1024.
+    ``m_indptr[E]`` on are left as they were (uninitialised without ``out``).  ``out``: a
+    ``[capacity, H]`` buffer for the rows with ``capacity >= moe_capacity(T, top_k, E, align)``.
+    1 <= top_k <= 16, 1 <= E <= 1024.
 
     Differentiable in x (bf16, fp16, fp32): the gradient is :func:`moe_permute_backward`; padding
     rows' gradients are not read.  Tensors that require gradients are refused while a CUDA graph is
@@ -749,20 +751,19 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
     if not 1 <= E <= 1024 or not 1 <= align <= 4096:
         raise ValueError(f"num_experts = {E}, align = {align}: 1 <= num_experts <= 1024 and 1 <= align <= 4096 are required")
     capacity = moe_capacity(T, top_k, E, align)
-    record = torch.is_grad_enabled() and x.requires_grad
+    _same_device("x", x, topk_ids=topk_ids, out=out)
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out is not supported for an x that requires gradients")
+        _need_row_dtype(x, "x that requires gradients")
+        _refuse_recording_in_capture("moe_permute", "moe_permute_backward")
+        return MoePermutation(*_MoePermuteFn.apply(x, topk_ids, E, align, zero_padding, capacity))
     if out is None:
-        out = torch.empty((capacity, x.shape[1]), dtype=x.dtype, device=x.device)
+        out = x.new_empty((capacity, x.shape[1]))
     else:
         _need(out, "out", x.dtype, 2)
         if out.shape[0] < capacity or out.shape[1] != x.shape[1]:
             raise ValueError(f"out must be [capacity, H] with capacity >= {capacity} and H = {x.shape[1]}, got {tuple(out.shape)}")
-        if record:
-            raise ValueError("out is not supported for an x that requires gradients")
-    _same_device("x", x, topk_ids=topk_ids, out=out)
-    if record:
-        _need_row_dtype(x, "x that requires gradients")
-        _refuse_recording_in_capture("moe_permute", "moe_permute_backward")
-        return MoePermutation(*_MoePermuteFn.apply(x, topk_ids, E, align, zero_padding, out))
     return MoePermutation(*_moe_permute(x, topk_ids, E, align, zero_padding, out))
 
 
@@ -914,7 +915,7 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
     (activations; scales are column-major unless given).  ``block_rows=128``: a scale per 128 x 128
     block (weights).  Rule, in fp32: ``amax = max(max |x|, 2^-100)``, ``scale = amax / 448``,
     ``q = e4m3(x * (448 / amax))``, nearest even.  Finite values are expected: a NaN stays a NaN, an
-    infinity makes its group's scale infinite."""
+    infinity makes its group's scale infinite.  Not differentiable."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)
     if block_rows not in (1, 128):

@@ -79,7 +79,10 @@ def test_quantizer_strided_outputs_and_misaligned_input():
 
 
 NORM = [(1, 8, BF), (2, 128, BF), (16, 4096, BF), (7, 1000, HF), (3, 5, FP), (9, 131, BF), (4, 8192, FP), (5, 16384, BF),
-        (3, 16392, HF), (300, 264, BF), (2, 6144, HF), (11, 2056, FP)]
+        (3, 16392, HF), (300, 264, BF), (2, 6144, HF), (11, 2056, FP),
+        # many rows: a warp per row, and one, two and four chunks per warp, aligned and not
+        (1201, 200, BF), (1203, 205, HF), (1200, 512, FP), (1205, 500, BF), (1190, 1000, BF), (1187, 1001, FP),
+        (1184, 3000, HF), (1185, 4095, BF), (1186, 4104, BF), (1184, 8200, HF), (1184, 8199, BF)]
 
 
 @pytest.mark.parametrize("residual", [True, False])
