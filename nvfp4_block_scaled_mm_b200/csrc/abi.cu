@@ -746,19 +746,21 @@ nvfp4lora_status check_fp8_rows(const void* x, const uint8_t* q, const float* sc
 
 // ---- the 8-bit product ----
 
-template <OutType OT>
+template <OutType OT, int TN>
 nvfp4lora_status launch_fp8_pair(DeviceInfo* info, const uint8_t* a, const uint8_t* b, Fp8GemmArgs args, int64_t K,
                                  cudaStream_t stream) {
     nvfp4lora_status st;
-    auto kernel = fp8_gemm_pair_kernel<OT>;
-    constexpr int smem = Fp8Smem::DYN_BYTES;
+    auto kernel = fp8_gemm_pair_kernel<OT, TN>;
+    constexpr int smem = Fp8Smem<TN>::DYN_BYTES;
     if ((st = ensure_smem_attr(info, kernel, smem)) != NVFP4LORA_OK) return st;
-    static std::atomic<int> regs_ok{0};            // one per instantiation
-    if ((st = check_split_regs(kernel, kFp8RegsLaunch, regs_ok, "8-bit product")) != NVFP4LORA_OK) return st;
+    if constexpr (TN == 256) {
+        static std::atomic<int> regs_ok{0};        // one per instantiation
+        if ((st = check_split_regs(kernel, kFp8RegsLaunch, regs_ok, "8-bit product")) != NVFP4LORA_OK) return st;
+    }
     CUtensorMap tm_a, tm_b, tm_out;
     std::memset(&tm_out, 0, sizeof(tm_out));
     if ((st = encode_2d(&tm_a, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.M, 128, 128)) != NVFP4LORA_OK) return st;
-    if ((st = encode_2d(&tm_b, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.N, 128, 128)) != NVFP4LORA_OK) return st;
+    if ((st = encode_2d(&tm_b, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.N, 128, TN / 2)) != NVFP4LORA_OK) return st;
     constexpr int esize = OT == OutType::FP32 ? 4 : 2;
     args.vec_out = ((int64_t)args.N * esize) % 16 == 0 && aligned(args.out, 16);
     if (args.vec_out &&
@@ -769,7 +771,7 @@ nvfp4lora_status launch_fp8_pair(DeviceInfo* info, const uint8_t* a, const uint8
                         esize, args.N, args.M, 64 / esize, kFp8BoxRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != NVFP4LORA_OK)
         return st;
     args.m_tiles = (args.M + kFp8TileM - 1) / kFp8TileM;
-    args.n_tiles = (args.N + kFp8TileN - 1) / kFp8TileN;
+    args.n_tiles = (args.N + TN - 1) / TN;
     const int64_t tiles = (int64_t)args.m_tiles * args.n_tiles;
     if (tiles > INT32_MAX - info->sms)       // a tile index one wave past the last stays in int32
         return fail(NVFP4LORA_ERR_INVALID_ARG, "too many output tiles (M x N too large)");
@@ -830,6 +832,7 @@ nvfp4lora_status launch_fp8_splitk(DeviceInfo* info, const uint8_t* a, const uin
 struct Fp8Plan {
     bool pair;               // the SM-pair kernel
     int mt, splits;          // the split-K kernel's token tile and cluster size
+    int tn;                  // the SM-pair kernel's tile columns
 };
 
 // The kernel of a shape.  Split-K kernel: the token tile is the smallest that holds M (128 from 65 rows on);
@@ -840,13 +843,14 @@ struct Fp8Plan {
 // Where 128-token tiles leave no SM free for a split, the SM-pair kernel is as fast or faster (300 x 4096 x
 // 4096: 19.1 us against 20.2; 200 x 4096 x 4096 splits 2-way: 15.1 against 18.9; 512 x 14336 x 4096: 36 against 78).
 Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t kblocks, int sms) {
-    Fp8Plan p{false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1};
+    Fp8Plan p{false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1, 256};
     const int64_t tiles = (N + 127) / 128 * ((M + p.mt - 1) / p.mt);
     const int64_t slots = p.mt <= 64 ? 2 * (int64_t)sms : sms;
     while (2 * p.splits <= kSplitMaxS && 2 * p.splits <= kblocks && 2 * p.splits * tiles <= slots &&
            (2 * p.splits * tiles <= sms || kblocks / p.splits >= 16))
         p.splits *= 2;
     p.pair = p.mt == 128 && p.splits == 1;
+    if ((M + kFp8TileM - 1) / kFp8TileM * ((N + 127) / 128) <= sms / 2) p.tn = 128;
     return p;
 }
 
@@ -854,7 +858,8 @@ template <OutType OT>
 nvfp4lora_status launch_fp8(DeviceInfo* info, const uint8_t* a, const uint8_t* b, const Fp8GemmArgs& g, int64_t K,
                             cudaStream_t stream) {
     const Fp8Plan plan = plan_fp8(g.M, g.N, g.kblocks, info->sms);
-    if (plan.pair) return launch_fp8_pair<OT>(info, a, b, g, K, stream);
+    if (plan.pair) return plan.tn == 128 ? launch_fp8_pair<OT, 128>(info, a, b, g, K, stream)
+                                         : launch_fp8_pair<OT, 256>(info, a, b, g, K, stream);
     Fp8SplitArgs s;
     s.a_scale = g.a_scale;
     s.b_scale = g.b_scale;

@@ -17,6 +17,8 @@
 // columns, which see a single sb per K block).  Registers are split by warpgroup: the promotion warps
 // hold 128 fp32 sums each and read 16 columns at a time (with 32 the loop spilled: 2.2 ms against 1.5 at
 // 8192 x 28672 x 8192).
+// With few tiles (TN = 128) a tile is 256 x 128, so that twice as many SM pairs work: four products of 128 columns in
+// TMEM, 64 columns per promotion warp, no register split.
 // What bounds it: the promotion, not the tensor pipe.  A K block takes about 850 cycles without operand loads and
 // 950 to 1100 with them, against 512 of MMAs: a promotion warp needs about 410 for its 128 columns, 185 to see a
 // product that is ready and 260 for the rest of its loop.  8192 x 28672 x 8192 runs 1.5 to 1.6 ms in short runs
@@ -156,8 +158,6 @@ __device__ __forceinline__ void store_out_one(void* out, int64_t i, float v) {
 }
 
 constexpr int kFp8TileM = 256;           // per SM pair: 128 rows per CTA
-constexpr int kFp8TileN = 256;
-constexpr int kFp8Stages = 6;
 constexpr int kFp8Threads = 384;         // warpgroup 0: producer, MMA issuer; 1 and 2: promotion
 constexpr int kFp8EpiWarps = 8;
 constexpr int kFp8BoxRows = 32;
@@ -169,16 +169,20 @@ constexpr int kFp8RegsEpi = 216;
 static_assert(128 * kFp8RegsCtl + 256 * kFp8RegsEpi <= kFp8Threads * kFp8RegsLaunch,
               "register split exceeds the launch's register pool");
 
+// TN: columns of a tile, 256 or 128.
+template <int TN>
 struct Fp8Smem {
+    static constexpr int STAGES = TN == 256 ? 6 : 8;
+    static constexpr int PRODUCTS = 512 / TN;             // products of a K block in TMEM
     static constexpr int A_BYTES = 128 * 128;
-    static constexpr int B_BYTES = 128 * 128;
+    static constexpr int B_BYTES = TN / 2 * 128;
     static constexpr int STAGE_TX = A_BYTES + B_BYTES;    // per CTA, on the leader's barrier
     static constexpr int A_OFF = 0;
-    static constexpr int B_OFF = A_OFF + kFp8Stages * A_BYTES;
-    static constexpr int OUT_OFF = B_OFF + kFp8Stages * B_BYTES;
+    static constexpr int B_OFF = A_OFF + STAGES * A_BYTES;
+    static constexpr int OUT_OFF = B_OFF + STAGES * B_BYTES;
     static constexpr int BOX_BYTES = 64 * kFp8BoxRows;    // 32 columns of a 16-bit type, 16 of fp32
     static constexpr int BAR_OFF = OUT_OFF + kFp8EpiWarps * BOX_BYTES;
-    static constexpr int NUM_BARS = 2 * kFp8Stages + 4 + 1;            // full, empty, acc_full[2], acc_empty[2], drain
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * PRODUCTS + 1;    // full, empty, acc_full, acc_empty, drain
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int TOTAL = MISC_OFF + 16;
     static constexpr int DYN_BYTES = TOTAL + 1024;
@@ -198,12 +202,12 @@ __device__ __forceinline__ void fp8_tile(int tile, int m_tiles, int n_tiles, int
     m_blk = band * kFp8Band + r - n_blk * bm;
 }
 
-template <OutType OT>
+template <OutType OT, int TN>
 __global__ void __launch_bounds__(kFp8Threads, 1)
 fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_out, const Fp8GemmArgs args) {
-    using L = Fp8Smem;
-    constexpr uint32_t IDESC = idesc_e4m3_m(kFp8TileM, kFp8TileN);
+    using L = Fp8Smem<TN>;
+    constexpr uint32_t IDESC = idesc_e4m3_m(kFp8TileM, TN);
     constexpr uint16_t kBoth = 0x3;
     constexpr uint32_t kAll = 0xffffffffu;
 
@@ -211,10 +215,10 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);   // the leader's is used
-    uint64_t* empty = full + kFp8Stages;
-    uint64_t* acc_full = empty + kFp8Stages;       // [2] a K block's product is complete
-    uint64_t* acc_empty = acc_full + 2;            // [2] the leader's: both CTAs have read it
-    uint64_t* drain = acc_empty + 2;
+    uint64_t* empty = full + L::STAGES;
+    uint64_t* acc_full = empty + L::STAGES;        // a K block's product is complete
+    uint64_t* acc_empty = acc_full + L::PRODUCTS;  // the leader's: both CTAs have read it
+    uint64_t* drain = acc_empty + L::PRODUCTS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
 
@@ -228,11 +232,11 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
         prefetch_tensor_map(&tm_a);
         prefetch_tensor_map(&tm_b);
         if (args.vec_out) prefetch_tensor_map(&tm_out);
-        for (int s = 0; s < kFp8Stages; ++s) {
+        for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(&full[s], 1);                // the leader's expect_tx; bytes from both CTAs
             mbar_init(&empty[s], 1);               // the leader's multicast commit
         }
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < L::PRODUCTS; ++k) {
             mbar_init(&acc_full[k], 1);            // the leader's multicast commit
             mbar_init(&acc_empty[k], 2 * kFp8EpiWarps);
         }
@@ -254,7 +258,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
     grid_launch_dependents();
 
     if (warp < 4) {
-        reg_dealloc<kFp8RegsCtl>();
+        if constexpr (TN == 256) reg_dealloc<kFp8RegsCtl>();
         if (warp == 0 && lane == 0) {
             // ------------------------------- TMA producer (both CTAs) -------------------------------
             grid_dependency_wait();
@@ -265,14 +269,14 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                 int m_blk, n_blk;
                 fp8_tile(tile, args.m_tiles, args.n_tiles, m_blk, n_blk);
                 const int row_a = m_blk * kFp8TileM + (int)rank * 128;   // this CTA's A rows
-                const int row_b = n_blk * kFp8TileN + (int)rank * 128;   // and B half
+                const int row_b = n_blk * TN + (int)rank * (TN / 2);   // and B half
                 for (int kb = 0; kb < args.kblocks; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
                     const uint32_t lead_full = map_to_rank(smem_u32(&full[stage]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE_TX);
                     tma_load_2d_pair(smem + L::A_OFF + stage * L::A_BYTES, &tm_a, lead_full, kb * 128, row_a);
                     tma_load_2d_pair(smem + L::B_OFF + stage * L::B_BYTES, &tm_b, lead_full, kb * 128, row_b);
-                    if (++stage == kFp8Stages) { stage = 0; phase ^= 1; }
+                    if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
                 }
             }
         } else if (warp == 1 && rank == 0) {
@@ -283,9 +287,9 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
             bool ok = true;
             for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
                 for (int kb = 0; kb < args.kblocks; ++kb, ++g) {
-                    const uint32_t buf = g & 1;
+                    const uint32_t buf = g % L::PRODUCTS;
                     ok = mbar_wait_short(&full[stage], phase, abort_flag) &&
-                         mbar_wait_short(&acc_empty[buf], ((g >> 1) & 1) ^ 1, abort_flag);
+                         mbar_wait_short(&acc_empty[buf], ((g / L::PRODUCTS) & 1) ^ 1, abort_flag);
                     if (!__all_sync(kAll, ok)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(smem + L::A_OFF + stage * L::A_BYTES);
@@ -293,13 +297,13 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                     if (elect_one()) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            tc_mma_fp8_pair(tmem + buf * kFp8TileN, sdesc_sw128(a_addr + j * 32),
+                            tc_mma_fp8_pair(tmem + buf * TN, sdesc_sw128(a_addr + j * 32),
                                             sdesc_sw128(b_addr + j * 32), IDESC, j > 0 ? 1u : 0u);
                         tc_commit_pair_multicast(&acc_full[buf], kBoth);
                         tc_commit_pair_multicast(&empty[stage], kBoth);
                     }
                     __syncwarp();
-                    if (++stage == kFp8Stages) { stage = 0; phase ^= 1; }
+                    if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
                 }
             }
             if (!ok || *abort_flag) {
@@ -312,11 +316,11 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
         }
         __syncwarp();
     } else {
-        reg_alloc<kFp8RegsEpi>();
+        if constexpr (TN == 256) reg_alloc<kFp8RegsEpi>();
         // ------------------------------- promotion and epilogue (both CTAs) -------------------------------
         const int ew = warp - 4;                       // 0..7
         const int q = warp & 3;                        // TMEM lane quarter of this warp
-        const int h = ew >> 2;                         // which 128 of the 256 columns
+        const int h = ew >> 2;                         // which half of the tile's columns
         const uint32_t lane_off = (uint32_t)(q * 32) << 16;
         grid_dependency_wait();
         const uint32_t lead_acc_empty = map_to_rank(smem_u32(acc_empty), 0);
@@ -326,31 +330,31 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
             int m_blk, n_blk;
             fp8_tile(tile, args.m_tiles, args.n_tiles, m_blk, n_blk);
             const int row0 = m_blk * kFp8TileM + (int)rank * 128 + q * 32;   // this warp's 32 rows
-            const int col0 = n_blk * kFp8TileN + h * 128;
+            const int col0 = n_blk * TN + h * (TN / 2);
             const float* sa = args.a_scale + (int64_t)min(row0 + lane, args.M - 1) * args.stride_am;
             const float* sb = args.b_scale + (int64_t)min(col0 / 128, (args.N - 1) / 128) * args.kblocks;
-            float acc[128];
+            float acc[TN / 2];
 #pragma unroll
-            for (int k = 0; k < 128; ++k) acc[k] = 0.0f;
+            for (int k = 0; k < TN / 2; ++k) acc[k] = 0.0f;
             // the scales of the next block, loaded one block ahead; they are multiplied when used (a multiply
             // here would stall the warp on the loads)
             float sa_next = *sa, sb_next = *sb;
             for (int kb = 0; kb < args.kblocks; ++kb, ++g) {
-                const uint32_t buf = g & 1;
+                const uint32_t buf = g % L::PRODUCTS;
                 const uint64_t ss = dup2(sa_next * sb_next);
                 if (kb + 1 < args.kblocks) {
                     sa_next = sa[(kb + 1) * args.stride_ak];
                     sb_next = sb[kb + 1];
                 }
-                if (!__all_sync(kAll, mbar_wait_short(&acc_full[buf], (g >> 1) & 1, abort_flag))) { ok = false; break; }
+                if (!__all_sync(kAll, mbar_wait_short(&acc_full[buf], (g / L::PRODUCTS) & 1, abort_flag))) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t src = tmem + lane_off + buf * kFp8TileN + h * 128;
+                const uint32_t src = tmem + lane_off + buf * TN + h * (TN / 2);
                 uint32_t p[2][16];
                 tmem_load_16(src, p[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < TN / 32; ++c) {
                     tmem_load_wait();
-                    if (c < 7) tmem_load_16(src + 16 * (c + 1), p[(c + 1) & 1]);
+                    if (c < TN / 32 - 1) tmem_load_16(src + 16 * (c + 1), p[(c + 1) & 1]);
                     else {
                         tc_fence_before();
                         __syncwarp();
@@ -366,7 +370,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
             constexpr int COLS = 64 / (int)sizeof(E);
             uint8_t* box = smem + L::OUT_OFF + ew * L::BOX_BYTES;
 #pragma unroll
-            for (int x = 0; x < 128; x += COLS) {
+            for (int x = 0; x < TN / 2; x += COLS) {
                 if (col0 + x >= args.N) break;
                 if (args.bias != nullptr) {
 #pragma unroll
