@@ -840,8 +840,11 @@ struct Fp8Plan {
 // clusters of those sizes fill the GPU's processor clusters badly) while all CTAs are resident at once (a
 // second wave always lost: 64 x 8192 x 4096 12.2 us with 4-way clusters, 19.4 with 5) and either SMs are free or
 // a CTA still has 16 blocks to stream (16 x 4096 x 4096: 7.0 us 4-way, 7.4 8-way; 16 x 4096 x 14336: 14.3 and 13.2).
-// Where 128-token tiles leave no SM free for a split, the SM-pair kernel is as fast or faster (300 x 4096 x
-// 4096: 19.1 us against 20.2; 200 x 4096 x 4096 splits 2-way: 15.1 against 18.9; 512 x 14336 x 4096: 36 against 78).
+// With 128-token tiles the SM-pair kernel takes what cannot be split (300 x 4096 x 4096: 14.6 us against 20.3), and
+// what can be split only 2-way over fewer than 48 blocks: its time per block of K is the lower, 2-way splits halve
+// the blocks (256 x 4096 x 4096: 14.0 us against 15.5 2-way; x 14336: 39.1 against 34.5; 128 x 4096 x 4096, 4-way:
+// 13.9 against 11.7).  Its tiles are 128 columns wide while they fit the GPU in one wave (512 x 4096 x 4096: 14.8 us
+// against 19.6 with 256; 1536 x 2048 x 4096, 96 tiles of 128: 25.7 against 21.0).
 Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t kblocks, int sms) {
     Fp8Plan p{false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1, 256};
     const int64_t tiles = (N + 127) / 128 * ((M + p.mt - 1) / p.mt);
@@ -849,7 +852,7 @@ Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t kblocks, int sms) {
     while (2 * p.splits <= kSplitMaxS && 2 * p.splits <= kblocks && 2 * p.splits * tiles <= slots &&
            (2 * p.splits * tiles <= sms || kblocks / p.splits >= 16))
         p.splits *= 2;
-    p.pair = p.mt == 128 && p.splits == 1;
+    p.pair = p.mt == 128 && (p.splits == 1 || (p.splits == 2 && kblocks < 48));
     if ((M + kFp8TileM - 1) / kFp8TileM * ((N + 127) / 128) <= sms / 2) p.tn = 128;
     return p;
 }

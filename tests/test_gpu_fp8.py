@@ -153,7 +153,8 @@ def product_problem(M, N, K, seed, whole=False):
 # few rows (split K; 16, 32, 64 and 128 token columns, several token tiles), the SM pair, ragged everything
 MM = [(1, 1, 16), (1, 4096, 4096), (16, 384, 128), (17, 130, 144), (16, 1000, 2064), (33, 129, 400), (64, 300, 1024),
       (65, 257, 272), (100, 1028, 1040), (128, 512, 2048), (129, 100, 96), (200, 130, 4096), (300, 4100, 4112),
-      (257, 2057, 528), (512, 4096, 512), (1000, 5001, 208), (2048, 2304, 1152)]
+      (257, 2057, 528), (512, 4096, 512), (1000, 5001, 208), (2048, 2304, 1152), (65, 8200, 272),
+      (128, 8192, 528), (200, 4096, 6160), (513, 9475, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", MM)
