@@ -788,7 +788,7 @@ def _moe_unpermute(y, idx, topk_weights, out, name="y"):
         out = y.new_empty((T, H))
     else:
         _need(out, "out", y.dtype, 2)
-        if tuple(out.shape) != (T, H):
+        if out.shape != (T, H):
             raise ValueError(f"out must be [T, H] = [{T}, {H}], got {tuple(out.shape)}")
     _same_device(name, y, expanded_idx_to_permuted_idx=idx, topk_weights=topk_weights, out=out)
     _call(_lib.nvfp4lora_moe_unpermute, y.device, y.data_ptr(), y.shape[0], H, _ROW_DTYPES[y.dtype], idx.data_ptr(),
@@ -829,7 +829,7 @@ def moe_unpermute(y: torch.Tensor, permutation, topk_weights: Optional[torch.Ten
     """
     whole = isinstance(permutation, MoePermutation)
     idx = permutation.expanded_idx_to_permuted_idx if whole else permutation
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (y, topk_weights)):
+    if torch.is_grad_enabled() and (getattr(y, "requires_grad", False) or getattr(topk_weights, "requires_grad", False)):
         if not whole:
             raise ValueError("y or topk_weights requires gradients: pass the MoePermutation, whose tables the gradient needs")
         if out is not None:
@@ -866,14 +866,14 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
         if topk_weights.shape != idx.shape:
             raise ValueError(f"topk_weights must be [T, top_k] = {tuple(idx.shape)}, got {tuple(topk_weights.shape)}")
         _need(y, "y", grad_out.dtype, 2)
-        if tuple(y.shape) != (rows, H):
+        if y.shape != (rows, H):
             raise ValueError(f"y must be [rows, H] = [{rows}, {H}], got {tuple(y.shape)}")
         grad_weights = torch.empty((T, top_k), dtype=torch.float32, device=grad_out.device)
     if grad_rows is None:
         grad_rows = torch.empty((rows, H), dtype=grad_out.dtype, device=grad_out.device)
     else:
         _need(grad_rows, "grad_rows", grad_out.dtype, 2)
-        if tuple(grad_rows.shape) != (rows, H):
+        if grad_rows.shape != (rows, H):
             raise ValueError(f"grad_rows must be [rows, H] = [{rows}, {H}], got {tuple(grad_rows.shape)}")
     _same_device("grad_out", grad_out, y=y, expanded_idx_to_permuted_idx=idx, permuted_idx_to_expanded_idx=inv,
                  m_indptr=m_indptr, topk_weights=topk_weights, grad_rows=grad_rows)
@@ -895,14 +895,14 @@ def _fp8_outputs(x, block_rows, q, scales):
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     else:
         _need(q, "q", torch.float8_e4m3fn, 2)
-        if tuple(q.shape) != (rows, H):
+        if q.shape != (rows, H):
             raise ValueError(f"q must be [rows, H] = [{rows}, {H}], got {tuple(q.shape)}")
     if scales is None:
         # activations' scales column-major: the product reads consecutive rows' scales together
         strides = (1, shape[0]) if block_rows == 1 else (shape[1], 1)
         scales = x.new_empty_strided(shape, strides, dtype=torch.float32)
     elif (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or not scales.is_cuda
-          or tuple(scales.shape) != shape):
+          or scales.shape != shape):
         raise ValueError(f"scales must be a float32 CUDA tensor of shape {shape}")
     return q, scales
 
@@ -979,9 +979,9 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
         raise ValueError(f"a is [M, K] = {tuple(a.shape)} but b is {tuple(b.shape)}: K differs")
     if not isinstance(a_scale, torch.Tensor) or a_scale.dtype != torch.float32 or not a_scale.is_cuda:
         raise ValueError("a_scale must be a float32 CUDA tensor")
-    if tuple(a_scale.shape) != (M, G):
+    if a_scale.shape != (M, G):
         raise ValueError(f"a_scale must be [M, ceil(K / 128)] = [{M}, {G}], got {tuple(a_scale.shape)}")
-    if tuple(b_scale.shape) != (-(-N // 128), G):
+    if b_scale.shape != (-(-N // 128), G):
         raise ValueError(f"b_scale must be [ceil(N / 128), ceil(K / 128)] = [{-(-N // 128)}, {G}], got {tuple(b_scale.shape)}")
     if bias is not None:
         _need(bias, "bias", torch.bfloat16, 1)
@@ -993,7 +993,7 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
         out = a.new_empty((M, N), dtype=out_dtype)
     else:
         _need(out, "out", out_dtype, 2)
-        if tuple(out.shape) != (M, N):
+        if out.shape != (M, N):
             raise ValueError(f"out must be [M, N] = [{M}, {N}]")
     _same_device("a", a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
     sm, sk = a_scale.stride()
