@@ -705,6 +705,12 @@ def _refuse_recording_in_capture(name: str, instead: str) -> None:
                          f"captured: call it on detached tensors and capture {instead}")
 
 
+def _refuse_gradient_in_capture(name: str) -> None:
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError(f"the recorded gradient of {name} does not run while a CUDA graph is being captured: call "
+                         f"{name}_backward inside the capture")
+
+
 class _MoePermuteFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, topk_ids, num_experts, align, zero_padding, capacity):
@@ -717,6 +723,7 @@ class _MoePermuteFn(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_rows, *_):
+        _refuse_gradient_in_capture("moe_permute")
         (idx,) = ctx.saved_tensors
         return moe_permute_backward(grad_rows.contiguous(), idx), None, None, None, None, None
 
@@ -731,12 +738,13 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
     order (``t * top_k + j``) and is padded to a multiple of ``align`` rows (128 for the grouped
     call).  Padding rows are zeros, or left as they were with ``zero_padding=False``; rows from
     ``m_indptr[E]`` on are left as they were (uninitialised without ``out``).  ``out``: a
-    ``[capacity, H]`` buffer for the rows with ``capacity >= moe_capacity(T, top_k, E, align)``.
+    ``[capacity, H]`` buffer for the rows with ``capacity >= moe_capacity(T, top_k, E, align)``, apart
+    from x.
     1 <= top_k <= 16, 1 <= E <= 1024.
 
     Differentiable in x (bf16, fp16, fp32): the gradient is :func:`moe_permute_backward`; padding
-    rows' gradients are not read.  Tensors that require gradients are refused while a CUDA graph is
-    captured (capture the two functions on detached tensors instead).  An id >= num_experts is read
+    rows' gradients are not read.  Tensors that require gradients, and a recorded gradient's own pass, are
+    refused while a CUDA graph is captured (capture the two functions on detached tensors instead).  An id >= num_experts is read
     on the device: it counts as inactive and :func:`nvfp4lora_device_status` raises ValueError.
     """
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
@@ -806,6 +814,7 @@ class _MoeUnpermuteFn(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out):
+        _refuse_gradient_in_capture("moe_unpermute")
         y, w, m_indptr, idx, inv = ctx.saved_tensors
         # rows behind the last segment get no gradient: their memory is written by no kernel
         grad_rows = torch.zeros_like(y)
@@ -820,8 +829,8 @@ def moe_unpermute(y: torch.Tensor, permutation, topk_weights: Optional[torch.Ten
 
     y: bf16, fp16 or fp32 ``[rows, H]``; permutation: a :class:`MoePermutation`, or its
     ``expanded_idx_to_permuted_idx`` (int32 ``[T, top_k]``) alone; topk_weights: fp32 ``[T, top_k]``,
-    None for weights of 1.  An index >= rows is read on the device: it is left out and
-    :func:`nvfp4lora_device_status` raises ValueError.
+    None for weights of 1; out must not overlap y.  An index >= rows is read on the device: it is left
+    out and :func:`nvfp4lora_device_status` raises ValueError.
 
     Differentiable in y and topk_weights where the whole MoePermutation is given (its gradient,
     :func:`moe_unpermute_backward`, needs the tables); as for :func:`moe_permute`, not while a CUDA
@@ -848,8 +857,8 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
     ``grad_rows[idx[t, j]] = topk_weights[t, j] * grad_out[t]`` and ``grad_weights[t, j] = <grad_out[t],
     y[idx[t, j]]>`` (fp32; 0 for an inactive slot; None without weights, where y is not read and may be
     None).  Padding rows of the segments get zeros; rows from ``m_indptr[E]`` on are left as they were
-    in ``grad_rows`` (a ``[rows, H]`` buffer; uninitialised there when None).  The tables are those of
-    one :class:`MoePermutation`."""
+    in ``grad_rows`` (a ``[rows, H]`` buffer, which may be y itself; uninitialised there when None).  The
+    tables are those of one :class:`MoePermutation`."""
     _need_row_dtype(grad_out, "grad_out")
     _need(grad_out, "grad_out", grad_out.dtype, 2)
     idx, inv = expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx
@@ -937,8 +946,8 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
     ``y = h * rsqrt(mean(h^2) + eps) * weight``; returns ``(q, scales)`` of y as :func:`fp8_quantize`
     with ``block_rows=1`` gives them (from the unrounded y), the ``a`` and ``a_scale`` of
     :func:`mm_fp8`.  ``norm_out [rows, H]`` also receives y in x's type (a router or a LoRA down
-    projection reads it); it may be x itself.  x, weight ``[H]``, residual and norm_out share one type
-    (bf16, fp16 or fp32).  Not differentiable."""
+    projection reads it); x may be norm_out or residual itself.  x, weight ``[H]``, residual and norm_out
+    share one type (bf16, fp16 or fp32).  Not differentiable."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)
     H = x.shape[1]

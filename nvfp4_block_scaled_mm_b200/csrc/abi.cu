@@ -701,6 +701,12 @@ nvfp4lora_status check_routing(int64_t T, int64_t top_k, int64_t rows) {
     return NVFP4LORA_OK;
 }
 
+// Two buffers share bytes (a null one shares none).
+bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a && b && a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
+}
+
 bool valid_type(int32_t t) {
     return t == NVFP4LORA_DTYPE_BF16 || t == NVFP4LORA_DTYPE_FP16 || t == NVFP4LORA_DTYPE_FP32;
 }
@@ -1269,6 +1275,8 @@ nvfp4lora_status nvfp4lora_moe_permute(const void* x, int64_t num_tokens, int64_
     if (counted && (!workspace || workspace_bytes < ws || !aligned(workspace, 4)))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "workspace needs %lld bytes, 4-byte aligned (got %lld)", (long long)ws,
                     (long long)workspace_bytes);
+    if (overlap(x, num_tokens * row_bytes, rows, padded_rows * row_bytes))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "rows must not overlap x");
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
@@ -1321,6 +1329,8 @@ nvfp4lora_status nvfp4lora_moe_unpermute(const void* y, int64_t padded_rows, int
     const int es = type_bytes(dtype);
     if (!aligned(y, es) || !aligned(out, es) || !aligned(expanded_idx_to_permuted_idx, 4) || !aligned(topk_weights, 4))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "y and out must be aligned to their elements, the tables 4-byte aligned");
+    if (overlap(y, padded_rows * H * es, out, num_tokens * H * es))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "out must not overlap y");
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
@@ -1381,6 +1391,10 @@ nvfp4lora_status nvfp4lora_moe_unpermute_backward(const void* grad_out, const vo
     if (!aligned(grad_out, es) || !aligned(y, es) || !aligned(grad_rows, es) || !aligned(expanded_idx_to_permuted_idx, 4) ||
         !aligned(permuted_idx_to_expanded_idx, 4) || !aligned(topk_weights, 4) || !aligned(grad_weights, 4))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "rows must be aligned to their elements, the tables 4-byte aligned");
+    const int64_t bytes = padded_rows * H * es;
+    if (overlap(grad_out, num_tokens * H * es, grad_rows, bytes) ||
+        (topk_weights && y != grad_rows && overlap(y, bytes, grad_rows, bytes)))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "grad_rows must not overlap grad_out, nor y unless it is y itself");
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
@@ -1455,6 +1469,10 @@ nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(const void* x, void* residual, c
     const int es = type_bytes(dtype);
     if (!aligned(residual, es) || !aligned(weight, es) || !aligned(norm_out, es))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "residual, weight and norm_out must be aligned to their elements");
+    const int64_t bytes = rows * H * es;
+    if (overlap(residual, bytes, norm_out, bytes) || (x != residual && overlap(x, bytes, residual, bytes)) ||
+        (x != norm_out && overlap(x, bytes, norm_out, bytes)))
+        return fail(NVFP4LORA_ERR_INVALID_ARG, "x, residual and norm_out must not overlap, but x may be one of the two");
     const int64_t groups = (H + 127) / 128;
     if ((st = check_scale_strides(rows, groups, scale_stride_row, scale_stride_group)) != NVFP4LORA_OK) return st;
     int dev = 0;

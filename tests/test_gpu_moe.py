@@ -287,6 +287,43 @@ def test_capture_replay_with_new_routing_and_refusal_of_recording():
     L.nvfp4lora_device_status()
 
 
+def test_recorded_gradients_are_refused_in_a_capture(monkeypatch):
+    import nvfp4_block_scaled_mm_b200 as L
+    T, k, E, H = 20, 2, 4, 32
+    leaf, w = rows_of(T, H, FP, 1).to(DEV).requires_grad_(), torch.rand(T, k, device=DEV)
+    p = L.moe_permute(leaf, routing(T, k, E, 1).to(DEV), E)
+    out = L.moe_unpermute(p.rows.detach().requires_grad_(), p, w)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(ValueError, match="moe_permute_backward"):
+        p.rows.sum().backward()
+    with pytest.raises(ValueError, match="moe_unpermute_backward"):
+        out.sum().backward()
+
+
+def test_buffers_that_overlap():
+    """The sort and the way back refuse to run in place; the gradient may replace y, x its own norm."""
+    import nvfp4_block_scaled_mm_b200 as L
+    x, ids = rows_of(40, 64, BF, 1).to(DEV), routing(40, 1, 4, 1).to(DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        L.moe_permute(x, ids, 4, align=1, out=x)
+    p = L.moe_permute(x, ids, 4, align=1)
+    with pytest.raises(ValueError, match="overlap"):
+        L.moe_unpermute(p.rows, p, out=p.rows)
+    with pytest.raises(ValueError, match="overlap"):
+        L.moe_unpermute_backward(x, None, p[2], p[3], p.m_indptr, grad_rows=x)
+    with pytest.raises(ValueError, match="overlap"):
+        L.add_rmsnorm_fp8_quantize(x, x[0].clone(), p.rows, norm_out=p.rows)
+    for T, k, H, dt in ((300, 8, 520, BF), (50, 16, 33, HF), (70, 3, 4096, FP)):
+        ids, w = routing(T, k, 8, 2).to(DEV), torch.rand(T, k, device=DEV)
+        p, g = L.moe_permute(rows_of(T, H, dt, 2).to(DEV), ids, 8), rows_of(T, H, dt, 3).to(DEV)
+        args = (p[2], p[3], p.m_indptr, w)
+        used = int(p.m_indptr[-1])
+        want = L.moe_unpermute_backward(g, p.rows, *args)
+        got = L.moe_unpermute_backward(g, p.rows, *args, grad_rows=p.rows)
+        assert got[0] is p.rows and torch.equal(got[0][:used], want[0][:used]) and torch.equal(got[1], want[1])
+    L.nvfp4lora_device_status()
+
+
 def test_side_stream_and_repeats_are_bitwise_equal():
     import nvfp4_block_scaled_mm_b200 as L
     ids, x = routing(5000, 8, 60, 3).to(DEV), rows_of(5000, 96, BF, 3).to(DEV)

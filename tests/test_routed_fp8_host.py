@@ -49,6 +49,7 @@ PERMUTE = dict(x=0x10000, T=100, row_bytes=64, ids=0x20000, k=4, E=8, align=128,
     (dict(inv=None), "non-null"), (dict(ids=0x20001), "4-byte aligned"),
     (dict(T=5000, cap=1 << 20), "workspace"), (dict(T=5000, cap=1 << 20, ws=0x70000, ws_bytes=64 * 8 * 4 - 1), "workspace"),
     (dict(T=1 << 29), "too large"), (dict(cap=1 << 31), "padded_rows"),
+    (dict(rows=0x10000), "overlap"), (dict(rows=0x118C0), "overlap"), (dict(x=0x45FFF), "overlap"),
 ])
 def test_permute_rules(lib, bad, word):
     assert word in refused(lib, lib.nvfp4lora_moe_permute, PERMUTE, bad)
@@ -61,6 +62,7 @@ UNPERMUTE = dict(y=0x10000, rows=512, H=64, dtype=0, idx=0x20000, w=0x30000, T=1
     (dict(T=-1), "num_tokens"), (dict(k=0), "top_k"), (dict(k=17), "top_k"), (dict(H=0), "H = 0"), (dict(dtype=3), "dtype"),
     (dict(dtype=-1), "dtype"), (dict(y=None), "non-null"), (dict(idx=None), "non-null"), (dict(out=None), "non-null"),
     (dict(y=0x10001), "aligned"), (dict(dtype=2, out=0x40002), "aligned"), (dict(w=0x30002), "aligned"), (dict(rows=-1), "padded_rows"),
+    (dict(out=0x10000), "overlap"), (dict(out=0x1FFFE), "overlap"), (dict(y=0x431FE), "overlap"),
 ])
 def test_unpermute_rules(lib, bad, word):
     assert word in refused(lib, lib.nvfp4lora_moe_unpermute, UNPERMUTE, bad)
@@ -77,6 +79,7 @@ BACKWARD = dict(g=0x10000, y=0x18000, rows=512, H=64, dtype=0, idx=0x20000, inv=
     (dict(k=17), "top_k"), (dict(H=0), "H = 0"), (dict(dtype=7), "dtype"), (dict(E=0), "num_experts"), (dict(gw=None), "go together"),
     (dict(w=None), "go together"), (dict(indptr=None), "m_indptr"), (dict(g=None), "non-null"), (dict(y=None), "non-null"),
     (dict(inv=None), "non-null"), (dict(gy=None), "non-null"), (dict(gy=0x40001), "aligned"), (dict(rows=0), "padded_rows"),
+    (dict(g=0x40000), "overlap"), (dict(g=0x4FFFE), "overlap"), (dict(y=0x40010), "overlap"),
 ])
 def test_unpermute_backward_rules(lib, bad, word):
     assert word in refused(lib, lib.nvfp4lora_moe_unpermute_backward, BACKWARD, bad)
@@ -102,6 +105,7 @@ NORM = dict(x=0x10000, res=0x18000, weight=0x20000, rows=10, H=300, dtype=0, eps
 @pytest.mark.parametrize("bad,word", [
     (dict(weight=None), "weight"), (dict(eps=-1.0), "eps"), (dict(eps=float("nan")), "eps"), (dict(res=0x18001), "aligned"),
     (dict(norm=0x19001), "aligned"), (dict(rows=0), "rows >= 1"), (dict(sr=2), "overlap"),
+    (dict(norm=0x18000), "must not overlap"), (dict(norm=0x10010), "must not overlap"), (dict(res=0x10010), "must not overlap"),
 ])
 def test_norm_rules(lib, bad, word):
     assert word in refused(lib, lib.nvfp4lora_rmsnorm_fp8_quantize, NORM, bad)
