@@ -768,13 +768,14 @@ nvfp4lora_status launch_fp8_pair(DeviceInfo* info, const uint8_t* a, const uint8
     if ((st = encode_2d(&tm_a, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.M, 128, 128)) != NVFP4LORA_OK) return st;
     if ((st = encode_2d(&tm_b, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, args.N, 128, TN / 2)) != NVFP4LORA_OK) return st;
     constexpr int esize = OT == OutType::FP32 ? 4 : 2;
-    args.vec_out = ((int64_t)args.N * esize) % 16 == 0 && aligned(args.out, 16);
-    if (args.vec_out &&
+    args.out_bytes = 16;
+    while (((int64_t)args.N * esize) % args.out_bytes != 0 || !aligned(args.out, args.out_bytes)) args.out_bytes /= 2;
+    if (args.out_bytes == 16 &&
         (st = encode_2d(&tm_out, args.out,
                         OT == OutType::FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                             : OT == OutType::FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        esize, args.N, args.M, 64 / esize, kFp8BoxRows, CU_TENSOR_MAP_SWIZZLE_NONE)) != NVFP4LORA_OK)
+                        esize, args.N, args.M, 64 / esize, kFp8BoxRows, CU_TENSOR_MAP_SWIZZLE_64B)) != NVFP4LORA_OK)
         return st;
     args.m_tiles = (args.M + kFp8TileM - 1) / kFp8TileM;
     args.n_tiles = (args.N + TN - 1) / TN;

@@ -47,7 +47,7 @@ struct Fp8GemmArgs {
     int64_t stride_am, stride_ak;
     int M, N, kblocks;       // kblocks = ceil(K / 128)
     int m_tiles, n_tiles, num_tiles;
-    int vec_out;             // rows of out 16-byte aligned: TMA stores
+    int out_bytes;           // alignment of out's rows: 16 (TMA stores), 8, 4 or 2 bytes
 };
 
 // Instruction descriptor: kind::f8f6f4, E4M3 x E4M3 -> fp32, K-major A and B.
@@ -181,7 +181,7 @@ struct Fp8Smem {
     static constexpr int B_OFF = A_OFF + STAGES * A_BYTES;
     static constexpr int OUT_OFF = B_OFF + STAGES * B_BYTES;
     static constexpr int BOX_BYTES = 64 * kFp8BoxRows;    // 32 columns of a 16-bit type, 16 of fp32
-    static constexpr int BAR_OFF = OUT_OFF + kFp8EpiWarps * BOX_BYTES;
+    static constexpr int BAR_OFF = OUT_OFF + kFp8EpiWarps * 2 * BOX_BYTES;
     static constexpr int NUM_BARS = 2 * STAGES + 2 * PRODUCTS + 1;    // full, empty, acc_full, acc_empty, drain
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int TOTAL = MISC_OFF + 16;
@@ -200,6 +200,22 @@ __device__ __forceinline__ void fp8_tile(int tile, int m_tiles, int n_tiles, int
     const int bm = min(kFp8Band, m_tiles - band * kFp8Band);
     n_blk = r / bm;
     m_blk = band * kFp8Band + r - n_blk * bm;
+}
+
+// Byte `at` of row r in a box of 32 rows of 64 bytes.
+__device__ __forceinline__ int fp8_box_at(int r, int at) { return r * 64 + (at ^ ((r >> 1 & 3) << 4)); }
+
+// The part of a box that lies in out (rows x cols elements from `out` on), a vector V of its rows' alignment per lane
+// (6606 x 21984 x 1472: 236 us with TMA stores; 280 with 4 bytes per lane at N = 21986, 359 with 2 at 21987;
+// 300 x 4100 x 4112, 8 bytes: 15.1 us, 16.9 with one element per lane).
+template <typename V, typename E>
+__device__ __forceinline__ void fp8_store_box(const uint8_t* box, E* out, int64_t N, int rows, int cols, int lane) {
+    constexpr int PER = 64 / (int)sizeof(V), STEP = 32 / PER;      // lanes per row, rows per step
+    const int at = lane % PER * (int)sizeof(V), c = at / (int)sizeof(E);
+    if (c >= cols) return;
+#pragma unroll 4
+    for (int r = lane / PER; r < 32; r += STEP)
+        if (r < rows) *reinterpret_cast<V*>(out + r * N + c) = *reinterpret_cast<const V*>(box + fp8_box_at(r, at));
 }
 
 // The K block that a tile starts with; it goes on around the end.  Tiles that run at one time and share an operand
@@ -238,7 +254,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
     if (threadIdx.x == 0) {
         prefetch_tensor_map(&tm_a);
         prefetch_tensor_map(&tm_b);
-        if (args.vec_out) prefetch_tensor_map(&tm_out);
+        if (args.out_bytes == 16) prefetch_tensor_map(&tm_out);
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(&full[s], 1);                // the leader's expect_tx; bytes from both CTAs
             mbar_init(&empty[s], 1);               // the leader's multicast commit
@@ -376,51 +392,64 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                 }
             }
             if (!ok) break;
-            // 64 bytes of each of the warp's 32 rows at a time through its box in shared memory
+            // 64 bytes of each of the warp's 32 rows at a time through its two boxes in shared memory, in turn.  The
+            // 16-byte parts of a row are swizzled by its number (SWIZZLE_64B), so that eight lanes' rows meet no
+            // bank twice.
             using E = typename std::conditional<OT == OutType::FP32, uint32_t, uint16_t>::type;
             constexpr int COLS = 64 / (int)sizeof(E);
-            uint8_t* box = smem + L::OUT_OFF + ew * L::BOX_BYTES;
+            if (args.out_bytes == 16 && lane == 0) bulk_wait_group_read<0>();   // the last tile's stores have read the boxes
+            if (args.bias != nullptr) {
+                // through the boxes, so that a thread reads four columns' values at a time
+                __syncwarp();
+                float* bias = reinterpret_cast<float*>(smem + L::OUT_OFF + ew * 2 * L::BOX_BYTES);
+                for (int k = lane; k < TN / 2; k += 32)
+                    bias[k] = __uint_as_float((uint32_t)args.bias[min(col0 + k, args.N - 1)] << 16);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < TN / 2; k += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(bias + k);
+                    acc[k] = __fadd_rn(acc[k], v.x);
+                    acc[k + 1] = __fadd_rn(acc[k + 1], v.y);
+                    acc[k + 2] = __fadd_rn(acc[k + 2], v.z);
+                    acc[k + 3] = __fadd_rn(acc[k + 3], v.w);
+                }
+            }
 #pragma unroll
             for (int x = 0; x < TN / 2; x += COLS) {
-                if (col0 + x >= args.N) break;
-                if (args.bias != nullptr) {
-#pragma unroll
-                    for (int k = 0; k < COLS; ++k)
-                        acc[x + k] = __fadd_rn(acc[x + k], __uint_as_float((uint32_t)args.bias[min(col0 + x + k, args.N - 1)] << 16));
-                }
-                if (args.vec_out && lane == 0) bulk_wait_group_read<0>();   // its previous store has read the box
+                if (col0 + x >= args.N || row0 >= args.M) break;
+                uint8_t* box = smem + L::OUT_OFF + (ew * 2 + (x / COLS) % 2) * L::BOX_BYTES;
+                if (x > 0 && args.out_bytes == 16 && lane == 0) bulk_wait_group_read<1>();   // the box's previous store has read it
                 __syncwarp();
-                uint4* dst = reinterpret_cast<uint4*>(box + lane * 64);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float* v = acc + x + k * (COLS / 4);
+                    uint4* dst = reinterpret_cast<uint4*>(box + fp8_box_at(lane, k * 16));
                     if constexpr (OT == OutType::FP32)
-                        dst[k] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                            __float_as_uint(v[3]));
+                        *dst = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                          __float_as_uint(v[3]));
                     else
-                        dst[k] = make_uint4(pack_out2<OT>(v[0], v[1]), pack_out2<OT>(v[2], v[3]),
-                                            pack_out2<OT>(v[4], v[5]), pack_out2<OT>(v[6], v[7]));
+                        *dst = make_uint4(pack_out2<OT>(v[0], v[1]), pack_out2<OT>(v[2], v[3]),
+                                          pack_out2<OT>(v[4], v[5]), pack_out2<OT>(v[6], v[7]));
                 }
-                if (args.vec_out) {
+                if (args.out_bytes == 16) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && row0 < args.M) {
+                    if (lane == 0) {
                         tma_store_2d(&tm_out, box, col0 + x, row0);
                         bulk_commit_group();
                     }
                 } else {
                     // rows of out off their 16-byte boundaries: neighbouring lanes store neighbouring columns
                     __syncwarp();
-                    const int cx = lane % COLS, n = col0 + x + cx;
-                    if (n < args.N)
-                        for (int r = lane / COLS; r < 32 && row0 + r < args.M; r += 32 / COLS)
-                            static_cast<E*>(args.out)[(int64_t)(row0 + r) * args.N + n] =
-                                reinterpret_cast<const E*>(box)[r * COLS + cx];
-                    __syncwarp();
+                    E* out = static_cast<E*>(args.out) + (int64_t)row0 * args.N + col0 + x;
+                    const int rows = args.M - row0, cols = args.N - col0 - x;
+                    if (args.out_bytes == 8) fp8_store_box<uint2>(box, out, args.N, rows, cols, lane);
+                    else if (args.out_bytes == 4) fp8_store_box<uint32_t>(box, out, args.N, rows, cols, lane);
+                    else if constexpr (sizeof(E) == 2) fp8_store_box<uint16_t>(box, out, args.N, rows, cols, lane);
                 }
             }
         }
-        if (args.vec_out && lane == 0) bulk_wait_group_all();
+        if (args.out_bytes == 16 && lane == 0) bulk_wait_group_all();
     }
 
     // Neither CTA leaves (or gives TMEM back) while the other may still reach its barriers or the
