@@ -1499,12 +1499,13 @@ nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(const void* x, void* residual, c
         // longer rows than the registers of a CTA hold are read twice
         if (H > kNormMaxThreads * 8 * 4) return launch_dependent("norm launch", row_fp8_kernel<TY, true>, rows, 256, s, a);
         // Chunks per warp: few where there are few rows, so that a row's latency is spread over many warps (16 x
-        // 4096: 1.96 us with one, 2.3 with two), and for short rows (4096 x 4096: 20.1 us with two, 22.7 with four);
-        // four for long ones, so that more rows are in flight per SM (8192 x 8192: 77 us with four, 87 with two).
-        // Four chunks of element accesses do not fit the registers of two CTAs.
+        // 4096: 1.93 us with one, 2.3 with two); otherwise two, which divide once for both (8192 x 2048: 13.4 us with
+        // two, 16.5 with one), and four for long rows: from 4096 on without a residual (7866 x 7168: 42 us with four,
+        // 46 with two), from 8192 on with one (3000 x 8192: 31 with four, 28.7 with two).  Four chunks of element
+        // accesses do not fit the registers of two CTAs.
         const bool few = rows < 8 * (int64_t)info->sms;
         if (H <= 512 && !few) {
-            // a warp per row: 65536 x 512 43 us, 68 with a CTA of two warps per row
+            // a warp per row: 65536 x 512 36 us, 68 with a CTA of two warps per row
             const int64_t grid = (rows + kNormShortRows - 1) / kNormShortRows;
             if (H <= 256)
                 return vec ? launch_dependent("norm launch", rmsnorm_fp8_kernel<TY, 1, true, true>, grid, 32 * kNormShortRows, s, a)
@@ -1512,8 +1513,8 @@ nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(const void* x, void* residual, c
             return vec ? launch_dependent("norm launch", rmsnorm_fp8_kernel<TY, 2, true, true>, grid, 32 * kNormShortRows, s, a)
                        : launch_dependent("norm launch", rmsnorm_fp8_kernel<TY, 2, false, true>, grid, 32 * kNormShortRows, s, a);
         }
-        const int64_t one = few ? kNormMaxThreads * 8 : 2048;
-        const int64_t two = few || !vec ? kNormMaxThreads * 16 : 4096;
+        const int64_t one = few ? kNormMaxThreads * 8 : vec ? 768 : 2048;
+        const int64_t two = few || !vec || residual ? kNormMaxThreads * 16 : 4096;
         const int per = H <= one ? 1 : H <= two ? 2 : 4;
         const int threads = (int)((H + 256 * per - 1) / (256 * per)) * 32;
         auto go = [&](auto kernel) { return launch_dependent("norm launch", kernel, rows, threads, s, a); };

@@ -10,8 +10,8 @@
 // the only rounding to fewer bits on its path.
 // A NaN stays a NaN in q and is ignored by amax; an infinity makes its group's scale infinite.
 //
-// HBM-bound: the norm of 8192 x 8192 bf16 with residual and the normed rows kept runs 95 us (6.4 TB/s), of 65536 x 512
-// 37 us (6.4); the quantizer of 8192 x 8192 37 us by rows (5.5) and of 28672 x 8192 102 us by blocks (6.9, part of the
+// HBM-bound: the norm of 8192 x 8192 bf16 with residual and the normed rows kept runs 92 us (6.6 TB/s), of 65536 x 512
+// 36 us (6.5); without either, where it moves 3 bytes per element, it is bound by instruction issue (46 us, 4.4).  The quantizer of 8192 x 8192 37 us by rows (5.5) and of 28672 x 8192 102 us by blocks (6.9, part of the
 // writes still in L2).  Sixteen rows take 2 us, launch latency.
 #pragma once
 
@@ -46,9 +46,41 @@ __device__ __forceinline__ uint32_t e4m3x2_rn(float a, float b) {
     return two;
 }
 
+// Packed fp32 arithmetic on eight values, each operation rounded to nearest even: half the instructions (the norm
+// is bound by instruction issue where it moves few bytes).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t d) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(d));
+    return v;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t fma2_rn(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint2 e4m3x8_scaled(const float (&y)[8], float inv) {
-    return make_uint2(e4m3x2_rn(y[0] * inv, y[1] * inv) | (e4m3x2_rn(y[2] * inv, y[3] * inv) << 16),
-                      e4m3x2_rn(y[4] * inv, y[5] * inv) | (e4m3x2_rn(y[6] * inv, y[7] * inv) << 16));
+    const uint64_t s = pack2(inv, inv);
+    uint32_t two[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2(mul2(pack2(y[2 * i], y[2 * i + 1]), s));
+        two[i] = e4m3x2_rn(v.x, v.y);
+    }
+    return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
 }
 
 __device__ __forceinline__ float abs_max8(const float (&y)[8]) {
@@ -88,7 +120,7 @@ __device__ __forceinline__ float cta_sum(float s, float* red) {
 constexpr int kNormShortRows = 8;          // rows (warps) of a SHORT CTA
 
 template <MoeType TY, int NV, bool VEC, bool SHORT>
-__global__ void __launch_bounds__(kNormMaxThreads, NV == 4 && VEC && !SHORT ? 2 : 0)
+__global__ void __launch_bounds__(kNormMaxThreads, SHORT || !VEC ? 0 : NV == 4 ? 2 : NV == 1 && TY != MoeType::FP32 ? 4 : 0)
 rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
     using C = RowChunk<TY, VEC>;
     __shared__ float red[32];
@@ -105,7 +137,7 @@ rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
     typename C::Raw wt[kLate ? 1 : NV];
     grid_dependency_wait();
     grid_launch_dependents();
-    float ss = 0.0f;
+    uint64_t ss2 = 0;                          // the even and the odd elements' sums
     {
         typename C::Raw xr[NV], rr[NV];
 #pragma unroll
@@ -126,9 +158,13 @@ rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
                 C::store(res, (int64_t)(warp + i * nw) * 256, H, lane, h[i]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);   // elements past H are 0
+            for (int e = 0; e < 8; e += 2) {   // elements past H are 0
+                const uint64_t v = pack2(h[i][e], h[i][e + 1]);
+                ss2 = fma2_rn(v, v, ss2);
+            }
         }
     }
+    float ss = unpack2(ss2).x + unpack2(ss2).y;
     if constexpr (SHORT) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
@@ -136,26 +172,28 @@ rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
         ss = cta_sum(ss, red);
     }
     const float rms = rsqrtf(ss / (float)H + a.eps);
+    float* sc = a.scales + row * a.stride_r;
+    uint8_t* q = a.q + row * H;
+    const uint64_t rms2 = pack2(rms, rms);
+    float mine = 1.0f;                         // VEC: lane i of a half-warp divides for its group of chunk i
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t e0 = (int64_t)(warp + i * nw) * 256;
-        float y[8];
-        if constexpr (!kLate) C::unpack(wt[i], y);
-        else C::unpack(C::load(a.weight, e0, H, lane), y);
+        float(&y)[8] = h[i];
+        float w[8];
+        if constexpr (!kLate) C::unpack(wt[i], w);
+        else C::unpack(C::load(a.weight, e0, H, lane), w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rms * y[e];
-        float* sc = a.scales + row * a.stride_r;
-        uint8_t* q = a.q + row * H;
+        for (int e = 0; e < 8; e += 2) {
+            const float2 v = unpack2(mul2(mul2(pack2(y[e], y[e + 1]), rms2), pack2(w[e], w[e + 1])));
+            y[e] = v.x;
+            y[e + 1] = v.y;
+        }
         if constexpr (VEC) {
             float m = abs_max8(y);
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            m = fmaxf(m, kFp8Tiny);
-            const int64_t at = e0 + lane * 8;
-            if (at < H) {
-                *reinterpret_cast<uint2*>(q + at) = e4m3x8_scaled(y, __fdiv_rn(kFp8Max, m));
-                if ((lane & 15) == 0) sc[at / 128 * a.stride_g] = __fdiv_rn(m, kFp8Max);
-            }
+            if (NV == 1 || (lane & 15) == i) mine = fmaxf(m, kFp8Tiny);
         } else {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -171,6 +209,17 @@ rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
             }
         }
         if (a.norm_out != nullptr) C::store(row_at<TY>(a.norm_out, row, H), e0, H, lane, y);
+    }
+    if constexpr (VEC) {
+        const float inv_mine = __fdiv_rn(kFp8Max, mine);
+        const int64_t g = (int64_t)(warp + (lane & 15) * nw) * 2 + (lane >> 4);
+        if ((lane & 15) < NV && g * 128 < H) sc[g * a.stride_g] = __fdiv_rn(mine, kFp8Max);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float inv = NV == 1 ? inv_mine : __shfl_sync(0xFFFFFFFFu, inv_mine, (lane & 16) + i);
+            const int64_t at = (int64_t)(warp + i * nw) * 256 + lane * 8;
+            if (at < H) *reinterpret_cast<uint2*>(q + at) = e4m3x8_scaled(h[i], inv);
+        }
     }
 }
 
