@@ -11,7 +11,7 @@
 // A NaN stays a NaN in q and is ignored by amax; an infinity makes its group's scale infinite.
 //
 // HBM-bound: the norm of 8192 x 8192 bf16 with residual and the normed rows kept runs 92 us (6.6 TB/s), of 65536 x 512
-// 36 us (6.5); without either, where it moves 3 bytes per element, it is bound by instruction issue (46 us, 4.4).  The quantizer of 8192 x 8192 37 us by rows (5.5) and of 28672 x 8192 102 us by blocks (6.9, part of the
+// 36 us (6.5); without either, where it moves 3 bytes per element, it is bound by instruction issue (46 us, 4.4).  The quantizer of 8192 x 8192 takes 32 us by rows (6.3) and of 28672 x 8192 102 us by blocks (6.9, part of the
 // writes still in L2).  Sixteen rows take 2 us, launch latency.
 #pragma once
 
@@ -88,6 +88,23 @@ __device__ __forceinline__ float abs_max8(const float (&y)[8]) {
 #pragma unroll
     for (int i = 2; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
     return m;
+}
+
+// Maxima of pairs of 16-bit values: the larger magnitude of a group is one of its values, so nothing is rounded, and
+// two rows' maxima are shuffled as one word.  A NaN is ignored, as by fmaxf.
+template <MoeType TY>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (TY == MoeType::BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Largest magnitudes of the even (low half) and the odd of eight 16-bit values.
+template <MoeType TY>
+__device__ __forceinline__ uint32_t abs_max_pairs(const uint4& w) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    return max2<TY>(max2<TY>(w.x & kAbs, w.y & kAbs), max2<TY>(w.z & kAbs, w.w & kAbs));
 }
 
 template <MoeType TY>
@@ -300,13 +317,17 @@ quantize_fp8_tile_kernel(const Fp8QuantArgs a) {
         if (c < nv && r0 + i * 16 < a.rows) raw[i] = R::load(a.x, ((r0 + i * 16) * nv + c) * 8, INT64_MAX, 0);
     if constexpr (BLOCK) {
         float m = 0.0f;
+        if constexpr (TY == MoeType::FP32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c < nv && r0 + i * 16 < a.rows) {
-                float y[8];
-                R::unpack(raw[i], y);
-                m = fmaxf(m, abs_max8(y));
-            }
+            for (int i = 0; i < 8; ++i)
+                if (c < nv && r0 + i * 16 < a.rows) m = fmaxf(m, abs_max8(raw[i].e));
+        } else {
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c < nv && r0 + i * 16 < a.rows) m2 = max2<TY>(m2, abs_max_pairs<TY>(raw[i].w[0]));
+            m = fmaxf(to_f32<TY>((uint16_t)m2), to_f32<TY>((uint16_t)(m2 >> 16)));
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
@@ -327,17 +348,25 @@ quantize_fp8_tile_kernel(const Fp8QuantArgs a) {
         // lane i of the sixteen divides for row i, once for all of them
         const int lane = threadIdx.x & 31, hl = threadIdx.x & 15;
         float mine = 1.0f;
+        if constexpr (TY == MoeType::FP32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float m = 0.0f;
-            if (c < nv && r0 + i * 16 < a.rows) {
-                float y[8];
-                R::unpack(raw[i], y);
-                m = abs_max8(y);
+            for (int i = 0; i < 8; ++i) {
+                float m = c < nv && r0 + i * 16 < a.rows ? abs_max8(raw[i].e) : 0.0f;
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                if (hl == i) mine = fmaxf(m, kFp8Tiny);
             }
+        } else {
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            if (hl == i) mine = fmaxf(m, kFp8Tiny);
+            for (int i = 0; i < 8; i += 2) {
+                const uint32_t u = c < nv && r0 + i * 16 < a.rows ? abs_max_pairs<TY>(raw[i].w[0]) : 0u;
+                const uint32_t v = c < nv && r0 + (i + 1) * 16 < a.rows ? abs_max_pairs<TY>(raw[i + 1].w[0]) : 0u;
+                // row i in the low half, row i + 1 in the high
+                uint32_t m2 = max2<TY>(__byte_perm(u, v, 0x5410), __byte_perm(u, v, 0x7632));
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) m2 = max2<TY>(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, d));
+                if ((hl & ~1) == i) mine = fmaxf(to_f32<TY>((uint16_t)(hl & 1 ? m2 >> 16 : m2)), kFp8Tiny);
+            }
         }
         const float inv_mine = __fdiv_rn(kFp8Max, mine);
         if (hl < 8 && r0 + hl * 16 < a.rows) a.scales[(r0 + hl * 16) * a.stride_r + bc * a.stride_g] = __fdiv_rn(mine, kFp8Max);

@@ -61,6 +61,31 @@ def test_quantizer_extremes():
     assert torch.isnan(last[3]) and last[4] == 448 and float(s[5, 0]) == np.float32(2) / np.float32(448)
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("H", [256, 254])            # packed maxima of aligned rows, and elements
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_quantizer_extremes_of_16_bit_types(dt, H, block_rows):
+    import nvfp4_block_scaled_mm_b200 as L
+    info = torch.finfo(dt)
+    sub = 2.0 ** (-133 if dt == BF else -24)         # the smallest subnormal
+    n = 5
+    x = torch.zeros(n * 128, H, dtype=dt)
+    b = [x[i * 128:(i + 1) * 128] for i in range(n)]  # a block of rows for each value
+    b[0][:, 1::2] = -sub
+    b[1][:, ::3] = info.max
+    b[2][:, 5] = -info.tiny
+    b[3][:] = randn(128, H, dtype=dt, seed=9)
+    b[3][7, :9] = float("nan")                       # in both halves of a pair, and beside the rows around it
+    b[3][7, 20] = -0.0
+    b[4][:] = float("nan")
+    q, s = L.fp8_quantize(x.to(DEV), block_rows=block_rows)
+    bad = torch.isnan(x)
+    wq, ws = R.fp8_quantize(torch.where(bad, torch.zeros_like(x), x).float().numpy(), block_rows)
+    assert np.array_equal(s.cpu().numpy(), ws)
+    assert torch.equal(torch.isnan(q.float().cpu()), bad)
+    assert np.array_equal(codes(q)[~bad.numpy()], wq[~bad.numpy()])
+
+
 def test_quantizer_strided_outputs_and_misaligned_input():
     import nvfp4_block_scaled_mm_b200 as L
     x = randn(50, 512, dtype=BF, seed=1).to(DEV)
