@@ -11,7 +11,8 @@
 // A NaN stays a NaN in q and is ignored by amax; an infinity makes its group's scale infinite.
 //
 // HBM-bound: the norm of 8192 x 8192 bf16 with residual and the normed rows kept runs 92 us (6.6 TB/s), of 65536 x 512
-// 36 us (6.5); without either, where it moves 3 bytes per element, it is bound by instruction issue (46 us, 4.4).  The quantizer of 8192 x 8192 takes 32 us by rows (6.3) and of 28672 x 8192 102 us by blocks (6.9, part of the
+// 36 us (6.5); without either, where it moves 3 bytes per element, it is bound by instruction issue (46 us, 4.4).
+// The quantizer of 8192 x 8192 takes 32 us by rows (6.3) and of 28672 x 8192 102 us by blocks (6.9, part of the
 // writes still in L2).  Sixteen rows take 2 us, launch latency.
 #pragma once
 
@@ -265,33 +266,48 @@ row_fp8_kernel(const Fp8QuantArgs a) {
         }
         rms = rsqrtf(cta_sum(ss, red) / (float)a.H + a.eps);
     }
-    const int64_t groups = (a.H + 127) / 128;
-    for (int64_t g = warp; g < groups; g += nw) {
-        float y[4], m = 0.0f;
+    const int H = (int)a.H, groups = (H + 127) / 128;
+    // Groups per warp at a time, their loads first and one division for all: 300 x 40001 normed 70 us with four, 100
+    // with one; without the norm's loads two are slower (11805 x 4570 60 us, 54 with one).
+    constexpr int NG = NORM ? 4 : 1;
+    for (int g0 = warp * NG; g0 < groups; g0 += nw * NG) {
+        float y[NG][4], mine = 1.0f;           // lane i divides for group g0 + i
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t i = g * 128 + e * 32 + lane;
-            y[e] = 0.0f;
-            if (i < a.H) {
-                y[e] = load_h(i);
-                if (NORM) {
-                    if (a.residual != nullptr) store_one<TY>(a.residual, base + i, y[e]);
-                    y[e] = y[e] * rms * load_one<TY>(a.weight, i);
-                    if (a.norm_out != nullptr) store_one<TY>(a.norm_out, base + i, y[e]);
-                }
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = (g0 + i) * 128 + e * 32 + lane;
+                y[i][e] = c < H ? load_h(c) : 0.0f;
             }
-            m = fmaxf(m, fabsf(y[e]));
-        }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        m = fmaxf(m, kFp8Tiny);
-        const float inv = __fdiv_rn(kFp8Max, m);
+        for (int i = 0; i < NG; ++i) {
+            float m = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t i = g * 128 + e * 32 + lane;
-            if (i < a.H) a.q[base + i] = (uint8_t)e4m3x2_rn(y[e] * inv, 0.0f);
+            for (int e = 0; e < 4; ++e) {
+                const int c = (g0 + i) * 128 + e * 32 + lane;
+                if (NORM && c < H) {
+                    if (a.residual != nullptr) store_one<TY>(a.residual, base + c, y[i][e]);
+                    y[i][e] = y[i][e] * rms * load_one<TY>(a.weight, c);
+                    if (a.norm_out != nullptr) store_one<TY>(a.norm_out, base + c, y[i][e]);
+                }
+                m = fmaxf(m, fabsf(y[i][e]));
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            if (NG == 1 || lane == i) mine = fmaxf(m, kFp8Tiny);
         }
-        if (lane == 0) a.scales[blockIdx.x * a.stride_r + g * a.stride_g] = __fdiv_rn(m, kFp8Max);
+        const float inv_mine = __fdiv_rn(kFp8Max, mine);
+        if (lane < NG && g0 + lane < groups)
+            a.scales[blockIdx.x * a.stride_r + (g0 + lane) * a.stride_g] = __fdiv_rn(mine, kFp8Max);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const float inv = NG == 1 ? inv_mine : __shfl_sync(0xFFFFFFFFu, inv_mine, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = (g0 + i) * 128 + e * 32 + lane;
+                if (c < H) a.q[base + c] = (uint8_t)e4m3x2_rn(y[i][e] * inv, 0.0f);
+            }
+        }
     }
 }
 
