@@ -402,8 +402,11 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                 // through the boxes, so that a thread reads four columns' values at a time
                 __syncwarp();
                 float* bias = reinterpret_cast<float*>(smem + L::OUT_OFF + ew * 2 * L::BOX_BYTES);
-                for (int k = lane; k < TN / 2; k += 32)
-                    bias[k] = __uint_as_float((uint32_t)args.bias[min(col0 + k, args.N - 1)] << 16);
+                uint32_t raw[TN / 64];                 // all loads before the first store
+#pragma unroll
+                for (int k = 0; k < TN / 64; ++k) raw[k] = args.bias[min(col0 + k * 32 + lane, args.N - 1)];
+#pragma unroll
+                for (int k = 0; k < TN / 64; ++k) bias[k * 32 + lane] = __uint_as_float(raw[k] << 16);
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < TN / 2; k += 4) {
