@@ -21,8 +21,8 @@
 // TMEM, 64 columns per promotion warp, no register split.
 // What bounds it: the promotion, not the tensor pipe.  A K block takes about 850 cycles without operand loads and
 // 950 to 1100 with them, against 512 of MMAs: a promotion warp needs about 410 for its 128 columns, 185 to see a
-// product that is ready and 260 for the rest of its loop.  8192 x 28672 x 8192 runs 1.5 to 1.6 ms in short runs
-// (2.4 to 2.6 PFLOP/s, 0.70 to 0.75 of twice the measured bf16 rate).  Products of 128 columns (four in TMEM) with two
+// product that is ready and 260 for the rest of its loop.  8192 x 28672 x 8192 runs 1.55 to 1.65 ms in short
+// runs (2.3 to 2.5 PFLOP/s, 0.68 to 0.72 of twice the measured bf16 rate).  Products of 128 columns (four in TMEM) with two
 // issuers, sixteen promotion warps of 64 columns, scales staged by a warp of their own and scales loaded two to four
 // blocks ahead all measured level or slower.
 #pragma once
