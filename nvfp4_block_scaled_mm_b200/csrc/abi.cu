@@ -701,10 +701,10 @@ nvfp4lora_status check_routing(int64_t T, int64_t top_k, int64_t rows) {
     return NVFP4LORA_OK;
 }
 
-// Two buffers share bytes (a null one shares none).
+// Two buffers share bytes (an empty or a null one shares none).
 bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a && b && a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
+    return a && b && np > 0 && nq > 0 && a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
 }
 
 bool valid_type(int32_t t) {
