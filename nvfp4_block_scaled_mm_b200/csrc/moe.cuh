@@ -279,13 +279,14 @@ __device__ __forceinline__ typename MoeElem<TY>::type from_f32(float f) {   // n
 }
 
 // A warp's share of a row: 256 elements from element e0 on, eight per lane.  VEC: the lane's eight are
-// neighbours, one 16-byte access (two for fp32); the row length is a multiple of 8 and rows start on
-// 16-byte boundaries.  Otherwise they are 32 apart, so that any alignment is read and written in
-// coalesced element accesses.
+// neighbours, one 16-byte access (two for fp32, each bounded by itself: a row of 12 ends between a lane's two);
+// rows are whole numbers of 16 bytes long and start on 16-byte boundaries.  Otherwise they are 32 apart, so that
+// any alignment is read and written in coalesced element accesses.
 template <MoeType TY, bool VEC>
 struct RowChunk {
     using E = typename MoeElem<TY>::type;
     static constexpr int NW = 8 * (int)sizeof(E) / 16;
+    static constexpr int PER = 16 / (int)sizeof(E);        // elements of a 16-byte access
     union Raw {
         uint4 w[NW];
         E e[8];
@@ -297,13 +298,9 @@ struct RowChunk {
         Raw r;
         const E* p = static_cast<const E*>(row);
         if constexpr (VEC) {
-            if (at(e0, lane, 0) < H) {
 #pragma unroll
-                for (int i = 0; i < NW; ++i) r.w[i] = reinterpret_cast<const uint4*>(p + at(e0, lane, 0))[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < NW; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < NW; ++i)
+                r.w[i] = at(e0, lane, i * PER) < H ? reinterpret_cast<const uint4*>(p + at(e0, lane, 0))[i] : make_uint4(0, 0, 0, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) r.e[i] = at(e0, lane, i) < H ? p[at(e0, lane, i)] : E(0);
@@ -337,10 +334,9 @@ struct RowChunk {
             r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
         }
         if constexpr (VEC) {
-            if (at(e0, lane, 0) < H) {
 #pragma unroll
-                for (int i = 0; i < NW; ++i) reinterpret_cast<uint4*>(p + at(e0, lane, 0))[i] = r.w[i];
-            }
+            for (int i = 0; i < NW; ++i)
+                if (at(e0, lane, i * PER) < H) reinterpret_cast<uint4*>(p + at(e0, lane, 0))[i] = r.w[i];
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

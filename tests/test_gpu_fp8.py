@@ -323,3 +323,30 @@ def test_outputs_past_32_bit_offsets():
     assert float(out[-1, -1]) == 16.0 and float(out[-3, -5]) == 16.0 and float(out[-4, -1]) == 0.0
     assert float(out.sum(dtype=torch.float64)) == 16.0 * 15
     L.nvfp4lora_device_status()
+
+
+@pytest.mark.parametrize("T", [1, 5, 1200])
+@pytest.mark.parametrize("H", [4, 12, 100, 260, 1004])
+def test_fp32_rows_of_four_modulo_eight(T, H):
+    """Quantizer and norm of fp32 rows that are whole 16-byte units but no multiple of eight elements: within their
+    row, and nothing written behind the last."""
+    import nvfp4_block_scaled_mm_b200 as L
+    x, r, w = randn(T, H, dtype=FP, seed=1), randn(T, H, dtype=FP, seed=2), 1 + 0.2 * randn(H, dtype=FP, seed=3)
+    q_all = torch.full((T * H + 64,), 3, dtype=torch.uint8, device=DEV)
+    q = q_all[:T * H].view(F8).view(T, H)
+    for block_rows in (1, 128):
+        _, s = L.fp8_quantize(x.to(DEV), block_rows=block_rows, q=q)
+        wq, ws = R.fp8_quantize(x.numpy(), block_rows)
+        assert np.array_equal(s.cpu().numpy(), ws) and np.array_equal(codes(q), wq) and torch.all(q_all[T * H:] == 3)
+    res_all = torch.full((T * H + 64,), 7.0, device=DEV)
+    out_all = res_all.clone()
+    res, out = res_all[:T * H].view(T, H), out_all[:T * H].view(T, H)
+    res.copy_(r)
+    L.add_rmsnorm_fp8_quantize(x.to(DEV), w.to(DEV), res, eps=1e-5, norm_out=out, q=q)
+    assert torch.equal(res.cpu(), x + r)
+    for whole in (res_all, out_all):
+        assert torch.all(whole[T * H:] == 7)
+    assert torch.all(q_all[T * H:] == 3)
+    _, ref = R.add_rmsnorm(f64(x), f64(r), f64(w), 1e-5)
+    rel = (H / 256 + 42) / 2 * 2.0 ** -24 + 12 * 2.0 ** -24
+    assert np.all(np.abs(f64(out) - ref) <= (2.0 ** -24 + rel) * np.abs(ref) + torch.finfo(FP).tiny)

@@ -428,3 +428,68 @@ def test_sorted_rows_into_the_lora_delta_replayed():
         for a, b in zip(got, want):
             assert torch.equal(a, b), seed
     L.nvfp4lora_device_status()
+
+
+def guarded(rows, H, dtype, fill, tail=64):
+    """A [rows, H] view and the whole buffer, whose last `tail` elements no call may touch."""
+    whole = torch.full((rows * H + tail,), fill, dtype=dtype, device=DEV)
+    return whole[:rows * H].view(rows, H), whole
+
+
+@pytest.mark.parametrize("T,k,E,align", [(1, 1, 1, 1), (1, 3, 2, 4), (37, 3, 5, 8), (300, 8, 16, 1)])
+@pytest.mark.parametrize("H,dt", [(4, FP), (12, FP), (100, FP), (252, FP), (260, FP), (1004, FP), (2052, FP), (4, BF), (12, HF), (100, BF)])
+def test_rows_that_end_inside_a_lanes_eight_elements(T, k, E, align, H, dt):
+    """Row lengths of 4 modulo 8: the last lane of a row holds four of its eight elements.  Sums, gradients and zeros
+    end with their row, in its middle and at the buffer's end, and nothing behind the last row is read into a result."""
+    import nvfp4_block_scaled_mm_b200 as L
+    ids = routing(T, k, E, T + H, 0.1 if T > 1 else 0.0)
+    cap = R.moe_capacity(T, k, E, align)
+    indptr, idx, inv = R.moe_tables(ids.numpy(), E, align, cap)
+    y, g = rows_of(cap, H, dt, 6), rows_of(T, H, dt, 7)
+    w = torch.rand(T, k, generator=torch.Generator().manual_seed(8))
+    y[torch.from_numpy(inv < 0)] = float("nan")
+    tables = [torch.as_tensor(t, dtype=torch.int32).to(DEV) for t in (idx, inv, indptr)]
+    yd, _ = guarded(cap, H, dt, float("nan"))
+    gd, _ = guarded(T, H, dt, float("nan"))
+    yd.copy_(y)
+    gd.copy_(g)
+    out, out_all = guarded(T, H, dt, 7.0)
+    gx, gx_all = guarded(T, H, dt, 7.0)
+    gy, gy_all = guarded(cap, H, dt, 7.0)
+    L.moe_unpermute(yd, tables[0], w.to(DEV), out=out)
+    L.moe_permute_backward(yd, tables[0], out=gx)
+    _, gw = L.moe_unpermute_backward(gd, yd, *tables, w.to(DEV), grad_rows=gy)
+    L.nvfp4lora_device_status()
+    for whole, n in ((out_all, T * H), (gx_all, T * H), (gy_all, cap * H)):
+        assert torch.all(whole[n:] == 7)
+    yn, gn, wn = f64(y), f64(g), f64(w)
+    for got, wt in ((out, wn), (gx, None)):
+        ref, mag = R.moe_sum(yn, idx, wt), R.moe_sum(np.abs(yn), idx, wt)
+        assert np.all(np.abs(f64(got) - ref) <= sum_tolerance(ref, mag, k, dt))
+    ry, rw = R.moe_unpermute_grads(gn, yn, idx, wn, np.full((cap, H), 7.0), int(indptr[-1]), inv)
+    assert np.all(np.abs(f64(gy) - ry) <= sum_tolerance(ry, np.abs(ry), 1, dt))
+    _, mw = R.moe_unpermute_grads(np.abs(gn), np.abs(yn), idx, wn, np.zeros((cap, H)), int(indptr[-1]), inv)
+    assert np.all(np.abs(f64(gw) - rw) <= max(H, 2) * 2.0 ** -24 * mw)
+    # the gradient in y's place reads the same rows that it writes
+    again, gw2 = L.moe_unpermute_backward(gd, yd, *tables, w.to(DEV), grad_rows=yd)
+    used = int(indptr[-1])
+    assert torch.equal(again[:used], gy[:used]) and torch.equal(gw, gw2)
+
+
+def test_gradients_of_fp32_rows_of_twelve_through_autograd():
+    import nvfp4_block_scaled_mm_b200 as L
+    T, k, E, H = 50, 2, 4, 12
+    ids, x = routing(T, k, E, 3), rows_of(T, H, FP, 3)
+    w = torch.rand(T, k, generator=torch.Generator().manual_seed(4))
+    c = rows_of(T, H, FP, 5)
+    xl, wl = x.to(DEV).requires_grad_(), w.to(DEV).requires_grad_()
+    p = L.moe_permute(xl, ids.to(DEV), E, align=4)
+    (L.moe_unpermute(p.rows * p.rows, p, wl) * c.to(DEV)).sum().backward()
+    # out = sum_j w_j x^2 over the active slots
+    xn, cn, wn = f64(x), f64(c), f64(w) * (ids >= 0).numpy()
+    gx = 2 * wn.sum(1, keepdims=True) * xn * cn
+    gw = (cn * xn * xn).sum(1, keepdims=True) * (ids >= 0).numpy()
+    mw = (np.abs(cn) * xn * xn).sum(1, keepdims=True) * (ids >= 0).numpy()
+    # x: k terms, four roundings each and k - 1 additions (all terms of one sign); w: H terms of three roundings
+    assert np.all(np.abs(f64(xl.grad) - gx) <= (4 + k) * 2.0 ** -24 * np.abs(gx))
+    assert np.all(np.abs(f64(wl.grad) - gw) <= (H + 4) * 2.0 ** -24 * mw)
