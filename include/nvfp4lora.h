@@ -370,7 +370,8 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_unpermute_backward(
  *   q       uint8 [rows, H]: E4M3 bytes.
  *   scales  fp32 [ceil(rows / block_rows), ceil(H / 128)], element (r, g) at
  *           r * scale_stride_row + g * scale_stride_group (row-major or column-major, no overlap).
- * rows >= 1, 1 <= H <= 2^20.  The pages have no counterpart.
+ * x, q and the scales' elements share no bytes with one another.  rows >= 1, 1 <= H <= 2^20.  The pages have no
+ * counterpart.
  */
 NVFP4LORA_API nvfp4lora_status nvfp4lora_fp8_quantize(
     const void* x, int64_t rows, int64_t H, int32_t dtype, int64_t block_rows,

@@ -924,7 +924,7 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
     (activations; scales are column-major unless given).  ``block_rows=128``: a scale per 128 x 128
     block (weights).  Rule, in fp32: ``amax = max(max |x|, 2^-100)``, ``scale = amax / 448``,
     ``q = e4m3(x * (448 / amax))``, nearest even.  Finite values are expected: a NaN stays a NaN, an
-    infinity makes its group's scale infinite.  Not differentiable."""
+    infinity makes its group's scale infinite.  q and scales must not overlap x or each other.  Not differentiable."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)
     if block_rows not in (1, 128):

@@ -707,6 +707,66 @@ bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
     return a && b && np > 0 && nq > 0 && a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
 }
 
+// A buffer and the fp32 elements (i, j) at `base` + i * si + j * sj, i < ni, j < nj, share bytes.  Exact where one
+// stride steps over all elements of the other (a matrix, its transpose, their slices), so that what lies in the gaps
+// between rows is told apart; elements that interleave in another way count as all bytes from the first to the last.
+bool overlap_elements(const void* p, int64_t np, const float* base, int64_t ni, int64_t si, int64_t nj, int64_t sj) {
+    using Wide = __int128;                       // strides are the caller's: no product of them overflows
+    if (!p || !base || np <= 0 || ni <= 0 || nj <= 0) return false;
+    if (ni == 1) si = 0;
+    if (nj == 1) sj = 0;
+    if (si < sj) { std::swap(si, sj); std::swap(ni, nj); }           // i: the outer dimension
+    Wide lo = (Wide)reinterpret_cast<uintptr_t>(p) - (Wide)reinterpret_cast<uintptr_t>(base), hi = lo + np;
+    // the first and the last of n pieces of `size` bytes, `step` apart, that [lo, hi) may share bytes with
+    auto pieces = [&](Wide n, Wide step, Wide size, Wide& first, Wide& last) {
+        auto floor_div = [](Wide a, Wide b) { return a >= 0 ? a / b : -((-a + b - 1) / b); };
+        first = step == 0 ? 0 : std::max<Wide>(0, floor_div(lo - size, step) + 1);
+        last = step == 0 ? 0 : std::min<Wide>(n - 1, floor_div(hi - 1, step));
+        return first <= last && lo < last * step + size && hi > first * step;
+    };
+    const Wide inner = 4 * ((Wide)(nj - 1) * sj + 1);
+    Wide first = 0, last = 0;
+    if (ni > 1 && 4 * (Wide)si < inner) return lo < inner + 4 * (Wide)(ni - 1) * si && hi > 0;
+    if (!pieces(ni, 4 * (Wide)si, inner, first, last)) return false;
+    if (first < last) return true;               // two rows' bytes: the second's first element lies between
+    lo -= first * 4 * si;
+    hi -= first * 4 * si;
+    return pieces(nj, 4 * (Wide)sj, 4, first, last);
+}
+
+// A contiguous buffer of a call, and fp32 scales of any strides.
+struct Span {
+    const char* name;
+    const void* p;
+    int64_t bytes;
+};
+struct Scales {
+    const char* name;
+    const float* p;
+    int64_t rows, stride_row, cols, stride_col;
+};
+
+// Blocks write their results while others still read: nothing that a call writes may share a byte with what it
+// reads, nor two of its results with each other.
+nvfp4lora_status check_apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span* w = written.begin(); w != written.end(); ++w) {
+        for (const Span& r : read)
+            if (overlap(w->p, w->bytes, r.p, r.bytes))
+                return fail(NVFP4LORA_ERR_INVALID_ARG, "%s must not overlap %s", w->name, r.name);
+        for (const Span* v = w + 1; v != written.end(); ++v)
+            if (overlap(w->p, w->bytes, v->p, v->bytes))
+                return fail(NVFP4LORA_ERR_INVALID_ARG, "%s must not overlap %s", w->name, v->name);
+    }
+    return NVFP4LORA_OK;
+}
+
+nvfp4lora_status check_apart(const Scales& s, std::initializer_list<Span> others) {
+    for (const Span& o : others)
+        if (overlap_elements(o.p, o.bytes, s.p, s.rows, s.stride_row, s.cols, s.stride_col))
+            return fail(NVFP4LORA_ERR_INVALID_ARG, "%s must not overlap %s", s.name, o.name);
+    return NVFP4LORA_OK;
+}
+
 bool valid_type(int32_t t) {
     return t == NVFP4LORA_DTYPE_BF16 || t == NVFP4LORA_DTYPE_FP16 || t == NVFP4LORA_DTYPE_FP32;
 }
@@ -1434,6 +1494,10 @@ nvfp4lora_status nvfp4lora_fp8_quantize(const void* x, int64_t rows, int64_t H, 
         return fail(NVFP4LORA_ERR_INVALID_ARG, "block_rows = %lld: 1 or 128 is required", (long long)block_rows);
     const int64_t groups = (H + 127) / 128, brows = (rows + block_rows - 1) / block_rows;
     if ((st = check_scale_strides(brows, groups, scale_stride_row, scale_stride_group)) != NVFP4LORA_OK) return st;
+    const Span sx{"x", x, rows * H * type_bytes(dtype)}, sq{"q", q, rows * H};
+    if ((st = check_apart({sq}, {sx})) != NVFP4LORA_OK ||
+        (st = check_apart(Scales{"scales", scales, brows, scale_stride_row, groups, scale_stride_group}, {sx, sq})) != NVFP4LORA_OK)
+        return st;
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;

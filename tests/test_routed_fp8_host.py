@@ -168,3 +168,55 @@ def test_oracle_norm_gradient_free_identities():
     x = rng.standard_normal((3, 40))
     h, y = R.add_rmsnorm(x, x, np.ones(40), 0.0)
     assert np.allclose(h, 2 * x) and np.allclose((y * y).mean(axis=1), 1.0)
+
+
+# bf16 x: 10 x 300 in [0x10000, 0x11770); q: [0x20000, 0x20BB8); scales (r, g) at r + 10 g: [0x30000, 0x30078)
+@pytest.mark.parametrize("bad", [
+    dict(q=0x10000), dict(q=0x1176F), dict(q=0x10000 - 2999), dict(x=0x20BB6), dict(scales=0x10000), dict(scales=0x1176C),
+    dict(scales=0x10000 - 116), dict(scales=0x20BB4), dict(scales=0x20000 - 116),
+    dict(scales=0x10000 - 400, sr=100, sg=1), dict(scales=0x20000 - 3612, sr=401, sg=200), dict(block_rows=128, scales=0x1176C, sr=3, sg=1),
+])
+def test_quantize_refuses_overlapping_buffers(lib, bad):
+    assert "must not overlap" in refused(lib, lib.nvfp4lora_fp8_quantize, QUANT, bad)
+
+
+def passes_the_host(f, ok, change):
+    """The call's own rules hold: without a GPU the next step finds no device."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where no kernel can be launched")
+    return f(*{**ok, **change}.values(), None) != 1
+
+
+@pytest.mark.parametrize("ok", [
+    dict(), dict(q=0x11770), dict(q=0x10000 - 3000), dict(scales=0x11770), dict(scales=0x10000 - 120), dict(scales=0x20BB8),
+    # scales (r, g) at r + 4000 g, a column of 40 bytes every 16000: x in the gap after the first, q after the second
+    dict(scales=0x10000 - 40, sg=4000, q=0x10000 + 16000), dict(scales=0x10000 - 0x100, sg=4000),
+    # scales two elements apart, a row of 20 bytes every 4000 (or 20000)
+    dict(scales=0x20000 - 20, sr=1000, sg=2), dict(scales=0x10000 - 20, sr=5000, sg=2),
+])
+def test_quantize_takes_buffers_side_by_side(lib, ok):
+    assert passes_the_host(lib.nvfp4lora_fp8_quantize, QUANT, ok)
+
+
+def test_overlap_of_strided_scales_by_brute_force(lib):
+    """Exact for matrices, transposes and their slices: against the sets of bytes."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where no kernel can be launched")
+    rng = np.random.default_rng(5)
+    seen = [0, 0]
+    for _ in range(4000):
+        rows, groups = int(rng.integers(1, 5)), int(rng.integers(1, 4))
+        H = 128 * (groups - 1) + 1
+        inner, outer = (rows, groups) if rng.random() < 0.5 else (groups, rows)
+        si = int(rng.integers(1, 4))
+        so = (inner - 1) * si + 1 + int(rng.integers(0, 400))
+        sr, sg = (si, so) if inner == rows else (so, si)
+        base, q = 0x100000, 0x100000 + 4 * int(rng.integers(-400, 1200))
+        x = 0x900000
+        bytes_s = {base + 4 * (r * sr + g * sg) + b for r in range(rows) for g in range(groups) for b in range(4)}
+        bytes_q = range(q, q + rows * H)
+        want = any(b in bytes_s for b in bytes_q)
+        args = dict(x=x, rows=rows, H=H, dtype=0, block_rows=1, q=q, scales=base, sr=sr, sg=sg)
+        assert (lib.nvfp4lora_fp8_quantize(*args.values(), None) == 1) == want, args
+        seen[want] += 1
+    assert min(seen) > 300
