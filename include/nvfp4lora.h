@@ -384,8 +384,8 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_fp8_quantize(
  *     y = h * (1 / sqrt(mean(h^2) + eps)) * weight;  norm_out <- round(y);
  *     (q, scales) as nvfp4lora_fp8_quantize with block_rows = 1 gives them for the unrounded y.
  * residual NULL: h = x, nothing is written back.  norm_out NULL: not written.  x, residual, weight [H]
- * and norm_out have one type `dtype`; x may be the buffer of norm_out or of residual, and the three share
- * no bytes otherwise.
+ * and norm_out have one type `dtype`; x may be the buffer of norm_out or of residual.  No other two of x,
+ * residual, weight, norm_out, q and the scales' elements share bytes, but x and weight, which are only read.
  */
 NVFP4LORA_API nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(
     const void* x, void* residual, const void* weight, int64_t rows, int64_t H, int32_t dtype, float eps,

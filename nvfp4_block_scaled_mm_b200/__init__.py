@@ -946,8 +946,8 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
     ``y = h * rsqrt(mean(h^2) + eps) * weight``; returns ``(q, scales)`` of y as :func:`fp8_quantize`
     with ``block_rows=1`` gives them (from the unrounded y), the ``a`` and ``a_scale`` of
     :func:`mm_fp8`.  ``norm_out [rows, H]`` also receives y in x's type (a router or a LoRA down
-    projection reads it); x may be norm_out or residual itself.  x, weight ``[H]``, residual and norm_out
-    share one type (bf16, fp16 or fp32).  Not differentiable."""
+    projection reads it); x may be norm_out or residual itself, and no other result overlaps another buffer of
+    the call.  x, weight ``[H]``, residual and norm_out share one type (bf16, fp16 or fp32).  Not differentiable."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)
     H = x.shape[1]

@@ -1534,12 +1534,16 @@ nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(const void* x, void* residual, c
     const int es = type_bytes(dtype);
     if (!aligned(residual, es) || !aligned(weight, es) || !aligned(norm_out, es))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "residual, weight and norm_out must be aligned to their elements");
-    const int64_t bytes = rows * H * es;
-    if (overlap(residual, bytes, norm_out, bytes) || (x != residual && overlap(x, bytes, residual, bytes)) ||
-        (x != norm_out && overlap(x, bytes, norm_out, bytes)))
-        return fail(NVFP4LORA_ERR_INVALID_ARG, "x, residual and norm_out must not overlap, but x may be one of the two");
     const int64_t groups = (H + 127) / 128;
     if ((st = check_scale_strides(rows, groups, scale_stride_row, scale_stride_group)) != NVFP4LORA_OK) return st;
+    // x may be residual or norm_out itself: a thread reads its elements before it writes them
+    const int64_t bytes = rows * H * es;
+    const Span sx{"x", x == residual || x == norm_out ? nullptr : x, bytes}, sr{"residual", residual, bytes},
+        sn{"norm_out", norm_out, bytes}, sw{"weight", weight, H * es}, sq{"q", q, rows * H};
+    if ((st = check_apart({sr, sn, sq}, {sx, sw})) != NVFP4LORA_OK ||
+        (st = check_apart(Scales{"scales", scales, rows, scale_stride_row, groups, scale_stride_group}, {sx, sr, sn, sw, sq})) !=
+            NVFP4LORA_OK)
+        return st;
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;

@@ -220,3 +220,26 @@ def test_overlap_of_strided_scales_by_brute_force(lib):
         assert (lib.nvfp4lora_fp8_quantize(*args.values(), None) == 1) == want, args
         seen[want] += 1
     assert min(seen) > 300
+
+
+# bf16 rows of 10 x 300 (0x1770 bytes): x 0x10000, residual 0x18000, norm_out 0x38000, q (0xBB8 bytes) 0x28000;
+# weight (0x258 bytes) 0x20000; scales (0x78 bytes) 0x30000
+NORMED = dict(NORM, norm=0x38000)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=0x10000), dict(q=0x1176F), dict(q=0x18000 - 2999), dict(q=0x3976F), dict(q=0x20257), dict(q=0x20000 - 2999),
+    dict(weight=0x18000 + 0x176E), dict(weight=0x38000 - 0x256), dict(weight=0x28000), dict(scales=0x1176C), dict(scales=0x18000 - 116),
+    dict(scales=0x38000), dict(scales=0x20254), dict(scales=0x28BB4), dict(x=0x28BB6), dict(x=0x18000, q=0x18000),
+    dict(x=0x38000, q=0x3976F), dict(x=0x18000, norm=0x18000),
+])
+def test_norm_refuses_overlapping_buffers(lib, bad):
+    assert "must not overlap" in refused(lib, lib.nvfp4lora_rmsnorm_fp8_quantize, NORMED, bad)
+
+
+@pytest.mark.parametrize("ok", [
+    dict(), dict(x=0x18000), dict(x=0x38000), dict(res=None, x=0x38000), dict(norm=None, x=0x18000), dict(weight=0x10000 + 600),
+    dict(q=0x11770, scales=0x10000 - 120, weight=0x19770), dict(res=None, norm=None), dict(q=0x10000 - 3000, norm=0x19770),
+])
+def test_norm_takes_buffers_side_by_side(lib, ok):
+    assert passes_the_host(lib.nvfp4lora_rmsnorm_fp8_quantize, NORMED, ok)
