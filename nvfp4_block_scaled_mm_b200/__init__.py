@@ -975,7 +975,7 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
 
     a: float8_e4m3fn ``[M, K]``; b: float8_e4m3fn ``[N, K]``; a_scale: fp32 ``[M, ceil(K / 128)]`` of any
     strides (column-major, as :func:`fp8_quantize` makes it, is read fastest); b_scale: fp32
-    ``[ceil(N / 128), ceil(K / 128)]`` contiguous; bias: bf16 ``[N]``.  K % 16 == 0; any M, N >= 1.  As for
+    ``[ceil(N / 128), ceil(K / 128)]`` contiguous; bias: bf16 ``[N]``; out overlaps none of them.  K % 16 == 0; any M, N >= 1.  As for
     :func:`mm_nvfp4_lora`, out is defined once a later :func:`nvfp4lora_device_status` has returned
     without raising ``DeviceTimeoutError``.  Not differentiable."""
     _need(a, "a", torch.float8_e4m3fn, 2)

@@ -1613,10 +1613,16 @@ nvfp4lora_status nvfp4lora_mm_fp8(const uint8_t* a, const uint8_t* b, const floa
         return fail(NVFP4LORA_ERR_INVALID_ARG, "out must be aligned to its elements and bias 2-byte aligned");
     if (a_scale_stride_m < 0 || a_scale_stride_k < 0)
         return fail(NVFP4LORA_ERR_INVALID_ARG, "a_scale strides must not be negative");
+    const int64_t kblocks = (K + 127) / 128;
+    const Span so{"out", out, M * N * type_bytes(out_dtype)};
+    nvfp4lora_status st = check_apart({so}, {{"a", a, M * K}, {"b", b, N * K}, {"b_scale", b_scale, (N + 127) / 128 * kblocks * 4},
+                                             {"bias", bias, N * 2}});
+    if (st != NVFP4LORA_OK ||
+        (st = check_apart(Scales{"a_scale", a_scale, M, a_scale_stride_m, kblocks, a_scale_stride_k}, {so})) != NVFP4LORA_OK)
+        return st;
     int dev = 0;
     DeviceInfo* info = nullptr;
-    nvfp4lora_status st = device_info(&dev, &info);
-    if (st != NVFP4LORA_OK) return st;
+    if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
     Fp8GemmArgs g = {};
     g.a_scale = a_scale;
     g.b_scale = b_scale;
@@ -1626,7 +1632,7 @@ nvfp4lora_status nvfp4lora_mm_fp8(const uint8_t* a, const uint8_t* b, const floa
     g.stride_ak = a_scale_stride_k;
     g.M = (int)M;
     g.N = (int)N;
-    g.kblocks = (int)((K + 127) / 128);
+    g.kblocks = (int)kblocks;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (out_dtype == NVFP4LORA_DTYPE_BF16) return launch_fp8<OutType::BF16>(info, a, b, g, K, s);
     if (out_dtype == NVFP4LORA_DTYPE_FP16) return launch_fp8<OutType::FP16>(info, a, b, g, K, s);

@@ -243,3 +243,26 @@ def test_norm_refuses_overlapping_buffers(lib, bad):
 ])
 def test_norm_takes_buffers_side_by_side(lib, ok):
     assert passes_the_host(lib.nvfp4lora_rmsnorm_fp8_quantize, NORMED, ok)
+
+
+# a 16 x 256 in [0x10000, 0x11000), b 256 x 256 in [0x20000, 0x30000), a_scale (m, kb) at m + 16 kb in [0x30000, 0x30080),
+# b_scale 2 x 2 in [0x40000, 0x40010), out bf16 16 x 256 (0x2000 bytes) at 0x50000, bias (0x200 bytes) at 0x60000
+PRODUCT = dict(MM, bias=0x60000)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(out=0x10000), dict(out=0x10FFE), dict(out=0x10000 - 0x1FFE), dict(out=0x2FFFE), dict(out=0x3007E), dict(out=0x30000 - 0x1FFE),
+    dict(out=0x4000E), dict(out=0x40000 - 0x1FFE), dict(out=0x601FE), dict(bias=0x51FFE), dict(dtype=2, bias=0x53FFE),
+    dict(sa=0x50000 - 0x100, sm=64, sk=1), dict(sa=0x51FFC, sm=0, sk=0), dict(sa=0x50000 - 120, sm=2, sk=1),
+])
+def test_mm_refuses_overlapping_buffers(lib, bad):
+    assert "must not overlap" in refused(lib, lib.nvfp4lora_mm_fp8, PRODUCT, bad)
+
+
+@pytest.mark.parametrize("ok", [
+    dict(), dict(a=0x20000), dict(out=0x11000), dict(out=0x10000 - 0x2000), dict(out=0x30080), dict(out=0x30000 + 0x10010),
+    dict(bias=0x52000), dict(bias=None), dict(sa=0x52000, sm=0, sk=0), dict(sa=0x50000 - 4, sm=0, sk=0),
+    dict(sa=0x50000 - 64, sk=4000), dict(sa=0x50000 - 8, sm=3000, sk=1),
+])
+def test_mm_takes_buffers_side_by_side(lib, ok):
+    assert passes_the_host(lib.nvfp4lora_mm_fp8, PRODUCT, ok)
