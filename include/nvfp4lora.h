@@ -306,12 +306,13 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_bgmv_moe_gemm2_lora_delta(
  * zero_padding == 0; rows from m_indptr[num_experts] on are left as they were.
  *   x        [num_tokens] rows of row_bytes bytes, contiguous; any element type (rows are copied).
  *   topk_ids int32 [num_tokens, top_k]; an expert may occur twice in a token's list.
- *   rows     [padded_rows] rows of row_bytes bytes, no byte of x among them; padded_rows must hold any routing of these sizes:
+ *   rows     [padded_rows] rows of row_bytes bytes; padded_rows must hold any routing of these sizes:
  *            floor((n + min(num_experts, n) * (align - 1)) / align) * align with n = num_tokens * top_k.
  *   m_indptr int32 [num_experts + 1]; expanded_idx_to_permuted_idx int32 [num_tokens * top_k];
  *   permuted_idx_to_expanded_idx int32 [padded_rows].
  *   workspace  4 * 64 * num_experts bytes when num_tokens * top_k > 4096 (else ignored, may be NULL);
  *            its contents need not be kept; two calls that may run at once need two.
+ * rows, the three tables and the workspace share no byte with x, topk_ids or one another.
  * Rules: 1 <= top_k <= 16, 1 <= num_experts <= 1024, 1 <= align <= 4096, num_tokens >= 0 (0 writes an
  * all-zero m_indptr and -1 entries).  Read on the device only: graph-capturable.  An expert id
  * >= num_experts is an inactive slot, and the next nvfp4lora_device_status returns
@@ -328,8 +329,8 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_permute(
  * Routed tokens, back: out[t] = sum_j topk_weights[t, j] * y[expanded_idx_to_permuted_idx[t, j]] over
  * the token's slots with an index >= 0 (zero when there is none), in fp32 in slot order, rounded once
  * to the rows' type.  topk_weights NULL: all weights 1.
- *   y [padded_rows, H], out [num_tokens, H] of `dtype` (bf16, fp16 or fp32), contiguous, apart from each
- *   other, aligned to their elements; expanded_idx_to_permuted_idx int32 and topk_weights fp32 [num_tokens, top_k].
+ *   y [padded_rows, H], out [num_tokens, H] of `dtype` (bf16, fp16 or fp32), contiguous, aligned to their
+ *   elements; expanded_idx_to_permuted_idx int32 and topk_weights fp32 [num_tokens, top_k].  out shares no byte with them.
  * An index >= padded_rows is left out, and the next nvfp4lora_device_status returns
  * NVFP4LORA_ERR_INVALID_ARG.  1 <= top_k <= 16, 1 <= H <= 2^20; num_tokens == 0 enqueues nothing.
  */
@@ -351,8 +352,8 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_permute_backward(
  *     grad_weights[t, j]   = sum_h grad_out[t, h] * y[row(t, j), h] (fp32; 0 for an inactive slot)
  * Padding rows of the segments get zeros; rows from m_indptr[num_experts] on are left as they were.
  * The tables are those that nvfp4lora_moe_permute wrote.  topk_weights and grad_weights may both be
- * NULL (weights 1; y is then not read and may be NULL).  grad_rows may be y itself, and shares no byte
- * with grad_out or y otherwise.  Rules as for nvfp4lora_moe_unpermute.
+ * NULL (weights 1; y is then not read and may be NULL).  grad_rows may be y itself; otherwise grad_rows and
+ * grad_weights share no byte with an input or each other.  Rules as for nvfp4lora_moe_unpermute.
  */
 NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_unpermute_backward(
     const void* grad_out, const void* y, int64_t padded_rows, int64_t H, int32_t dtype,

@@ -738,9 +738,8 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
     order (``t * top_k + j``) and is padded to a multiple of ``align`` rows (128 for the grouped
     call).  Padding rows are zeros, or left as they were with ``zero_padding=False``; rows from
     ``m_indptr[E]`` on are left as they were (uninitialised without ``out``).  ``out``: a
-    ``[capacity, H]`` buffer for the rows with ``capacity >= moe_capacity(T, top_k, E, align)``, apart
-    from x.
-    1 <= top_k <= 16, 1 <= E <= 1024.
+    ``[capacity, H]`` buffer for the rows with ``capacity >= moe_capacity(T, top_k, E, align)``; it must not
+    overlap x or topk_ids.  1 <= top_k <= 16, 1 <= E <= 1024.
 
     Differentiable in x (bf16, fp16, fp32): the gradient is :func:`moe_permute_backward`; padding
     rows' gradients are not read.  Tensors that require gradients, and a recorded gradient's own pass, are
@@ -829,7 +828,7 @@ def moe_unpermute(y: torch.Tensor, permutation, topk_weights: Optional[torch.Ten
 
     y: bf16, fp16 or fp32 ``[rows, H]``; permutation: a :class:`MoePermutation`, or its
     ``expanded_idx_to_permuted_idx`` (int32 ``[T, top_k]``) alone; topk_weights: fp32 ``[T, top_k]``,
-    None for weights of 1; out must not overlap y.  An index >= rows is read on the device: it is left
+    None for weights of 1; out must not overlap an input.  An index >= rows is read on the device: it is left
     out and :func:`nvfp4lora_device_status` raises ValueError.
 
     Differentiable in y and topk_weights where the whole MoePermutation is given (its gradient,
@@ -857,8 +856,8 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
     ``grad_rows[idx[t, j]] = topk_weights[t, j] * grad_out[t]`` and ``grad_weights[t, j] = <grad_out[t],
     y[idx[t, j]]>`` (fp32; 0 for an inactive slot; None without weights, where y is not read and may be
     None).  Padding rows of the segments get zeros; rows from ``m_indptr[E]`` on are left as they were
-    in ``grad_rows`` (a ``[rows, H]`` buffer, which may be y itself; uninitialised there when None).  The
-    tables are those of one :class:`MoePermutation`."""
+    in ``grad_rows`` (a ``[rows, H]`` buffer, which may be y itself and must not overlap an input otherwise;
+    uninitialised there when None).  The tables are those of one :class:`MoePermutation`."""
     _need_row_dtype(grad_out, "grad_out")
     _need(grad_out, "grad_out", grad_out.dtype, 2)
     idx, inv = expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx

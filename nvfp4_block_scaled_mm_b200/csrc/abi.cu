@@ -1336,8 +1336,12 @@ nvfp4lora_status nvfp4lora_moe_permute(const void* x, int64_t num_tokens, int64_
     if (counted && (!workspace || workspace_bytes < ws || !aligned(workspace, 4)))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "workspace needs %lld bytes, 4-byte aligned (got %lld)", (long long)ws,
                     (long long)workspace_bytes);
-    if (overlap(x, num_tokens * row_bytes, rows, padded_rows * row_bytes))
-        return fail(NVFP4LORA_ERR_INVALID_ARG, "rows must not overlap x");
+    if ((st = check_apart({{"rows", rows, padded_rows * row_bytes}, {"m_indptr", m_indptr, (num_experts + 1) * 4},
+                           {"expanded_idx_to_permuted_idx", expanded_idx_to_permuted_idx, n * 4},
+                           {"permuted_idx_to_expanded_idx", permuted_idx_to_expanded_idx, padded_rows * 4},
+                           {"workspace", workspace, ws}},
+                          {{"x", x, num_tokens * row_bytes}, {"topk_ids", topk_ids, n * 4}})) != NVFP4LORA_OK)
+        return st;
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
@@ -1390,8 +1394,11 @@ nvfp4lora_status nvfp4lora_moe_unpermute(const void* y, int64_t padded_rows, int
     const int es = type_bytes(dtype);
     if (!aligned(y, es) || !aligned(out, es) || !aligned(expanded_idx_to_permuted_idx, 4) || !aligned(topk_weights, 4))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "y and out must be aligned to their elements, the tables 4-byte aligned");
-    if (overlap(y, padded_rows * H * es, out, num_tokens * H * es))
-        return fail(NVFP4LORA_ERR_INVALID_ARG, "out must not overlap y");
+    const int64_t n = num_tokens * top_k;
+    if ((st = check_apart({{"out", out, num_tokens * H * es}},
+                          {{"y", y, padded_rows * H * es}, {"expanded_idx_to_permuted_idx", expanded_idx_to_permuted_idx, n * 4},
+                           {"topk_weights", topk_weights, n * 4}})) != NVFP4LORA_OK)
+        return st;
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;
@@ -1452,10 +1459,14 @@ nvfp4lora_status nvfp4lora_moe_unpermute_backward(const void* grad_out, const vo
     if (!aligned(grad_out, es) || !aligned(y, es) || !aligned(grad_rows, es) || !aligned(expanded_idx_to_permuted_idx, 4) ||
         !aligned(permuted_idx_to_expanded_idx, 4) || !aligned(topk_weights, 4) || !aligned(grad_weights, 4))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "rows must be aligned to their elements, the tables 4-byte aligned");
-    const int64_t bytes = padded_rows * H * es;
-    if (overlap(grad_out, num_tokens * H * es, grad_rows, bytes) ||
-        (topk_weights && y != grad_rows && overlap(y, bytes, grad_rows, bytes)))
-        return fail(NVFP4LORA_ERR_INVALID_ARG, "grad_rows must not overlap grad_out, nor y unless it is y itself");
+    // grad_rows may be y itself: a thread reads its elements before it writes them
+    const int64_t bytes = padded_rows * H * es, n = num_tokens * top_k;
+    if ((st = check_apart({{"grad_rows", grad_rows, bytes}, {"grad_weights", grad_weights, n * 4}},
+                          {{"grad_out", grad_out, num_tokens * H * es}, {"y", topk_weights && y != grad_rows ? y : nullptr, bytes},
+                           {"expanded_idx_to_permuted_idx", expanded_idx_to_permuted_idx, n * 4},
+                           {"permuted_idx_to_expanded_idx", permuted_idx_to_expanded_idx, padded_rows * 4},
+                           {"m_indptr", m_indptr, (num_experts + 1) * 4}, {"topk_weights", topk_weights, n * 4}})) != NVFP4LORA_OK)
+        return st;
     int dev = 0;
     DeviceInfo* info = nullptr;
     if ((st = device_info(&dev, &info)) != NVFP4LORA_OK) return st;

@@ -266,3 +266,49 @@ def test_mm_refuses_overlapping_buffers(lib, bad):
 ])
 def test_mm_takes_buffers_side_by_side(lib, ok):
     assert passes_the_host(lib.nvfp4lora_mm_fp8, PRODUCT, ok)
+
+
+# 5000 tokens, 4 slots, 8 experts, 1 byte per row: x 0x100000 (0x1388 bytes), ids 0x110000 (0x13880), rows 0x140000 (0x10000),
+# m_indptr 0x160000 (0x24), idx 0x170000 (0x13880), inv 0x1A0000 (0x40000), workspace 0x200000 (0x800)
+ROUTED = dict(x=0x100000, T=5000, row_bytes=1, ids=0x110000, k=4, E=8, align=128, zero=1, rows=0x140000, cap=0x10000,
+              indptr=0x160000, idx=0x170000, inv=0x1A0000, ws=0x200000, ws_bytes=0x800)
+# bf16 rows of 64: grad_out 0x100000 (0x3200), y 0x110000 (0x10000), idx 0x130000 (0x640), inv 0x140000 (0x800),
+# m_indptr 0x150000 (0x14), weights 0x160000 (0x640), grad_rows 0x170000 (0x10000), grad_weights 0x190000 (0x640)
+GRADS = dict(g=0x100000, y=0x110000, rows=512, H=64, dtype=0, idx=0x130000, inv=0x140000, indptr=0x150000, E=4, w=0x160000,
+             T=100, k=4, gy=0x170000, gw=0x190000)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=0x101387), dict(rows=0x110000), dict(indptr=0x101384), dict(indptr=0x14FFFC), dict(idx=0x11387C), dict(idx=0x160020),
+    dict(inv=0x100000), dict(inv=0x18387C), dict(inv=0x14FFFC), dict(ws=0x12387C), dict(ws=0x1DFFFC), dict(ws=0x160000), dict(x=0x200000),
+    dict(ids=0x1DFFFC), dict(ids=0x2007FC),
+])
+def test_permute_refuses_overlapping_tables(lib, bad):
+    assert "must not overlap" in refused(lib, lib.nvfp4lora_moe_permute, ROUTED, bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(idx=0x40000), dict(idx=0x431FC), dict(w=0x431FC), dict(out=0x30000 + 0x63E), dict(out=0x20000 - 0x31FE),
+])
+def test_unpermute_refuses_overlapping_tables(lib, bad):
+    assert "must not overlap" in refused(lib, lib.nvfp4lora_moe_unpermute, UNPERMUTE, bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(idx=0x17FFFC), dict(inv=0x170000), dict(indptr=0x17FFFC), dict(w=0x170000), dict(gw=0x17FFFC), dict(gw=0x130000),
+    dict(gw=0x1407FC), dict(gw=0x150010), dict(gw=0x160000), dict(gw=0x1031FC), dict(gw=0x11FFFC), dict(y=0x170000, gw=0x17FFFC),
+    dict(gw=None, w=None, indptr=0x170000),
+])
+def test_unpermute_backward_refuses_overlapping_tables(lib, bad):
+    assert "must not overlap" in refused(lib, lib.nvfp4lora_moe_unpermute_backward, GRADS, bad)
+
+
+def test_routed_calls_take_buffers_side_by_side(lib):
+    for f, base, oks in (
+            (lib.nvfp4lora_moe_permute, ROUTED, (dict(), dict(x=0x110000), dict(indptr=0x150000), dict(ws=0x1E0000), dict(rows=0x123880),
+                                                dict(T=100, ws=0x160000, ws_bytes=0x800))),       # a workspace that is not used
+            (lib.nvfp4lora_moe_unpermute, UNPERMUTE, (dict(), dict(w=None), dict(idx=0x43200), dict(w=0x20000))),
+            (lib.nvfp4lora_moe_unpermute_backward, GRADS, (dict(), dict(y=0x170000), dict(gw=None, w=None), dict(gw=None, w=None, y=0x170010),
+                                                           dict(gw=0x150014), dict(gw=0x180000), dict(y=0x180000)))):
+        for ok in oks:
+            assert passes_the_host(f, base, ok), (ok, lib.nvfp4lora_last_error())
