@@ -28,6 +28,7 @@ import os
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.graph import increment_version
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4lora.so")
 
@@ -161,6 +162,14 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _written(*tensors) -> None:
+    """Count a write by address in the version counters of the caller's buffers (None: not given), as an in-place
+    operation of torch does: autograd then refuses to use a saved tensor that a call has overwritten."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        increment_version(given)
+
+
 def _version_token(lora_b: torch.Tensor, lora_scale: torch.Tensor) -> int:
     return ((lora_b._version & 0xFFFFFFFF) << 32) | (lora_scale._version & 0xFFFFFFFF)
 
@@ -173,6 +182,7 @@ def nvfp4lora_mm(a, b, a_sf, b_sf, alpha, d, lora_b, lora_scale, r, bias, out, M
     _check(_lib.nvfp4lora_mm(_ptr(a), _ptr(b), _ptr(a_sf), a_sf.numel(), _ptr(b_sf), b_sf.numel(),
                              _ptr(alpha), _ptr(d), _ptr(lora_b), _ptr(lora_scale), int(r), _ptr(bias),
                              _ptr(out), int(M), int(N), int(K), _stream(stream)))
+    _written(out)
     return out
 
 
@@ -196,6 +206,7 @@ def nvfp4lora_mm_prepared(a, b, a_sf, b_sf, alpha, d, adp, cur_lora_b, cur_lora_
                                       b_sf.numel(), _ptr(alpha), _ptr(d), ctypes.byref(adp),
                                       _ptr(cur_lora_b), _ptr(cur_lora_scale), int(cur_version),
                                       _ptr(bias), _ptr(out), int(M), int(N), int(K), _stream(stream)))
+    _written(out)
     return out
 
 
@@ -205,6 +216,7 @@ def nvfp4lora_grouped_mm(a, b, a_sf, b_sf, m_indptr, num_experts, alpha, d, lora
                                      _ptr(m_indptr), int(num_experts), _ptr(alpha), _ptr(d), _ptr(lora_b),
                                      _ptr(lora_scale), int(r), _ptr(bias), _ptr(out), int(rows), int(N), int(K),
                                      _stream(stream)))
+    _written(out)
     return out
 
 
@@ -216,6 +228,7 @@ def nvfp4lora_bgmv_moe_gemm2_lora_delta(act, padded_rows, I, perm, w_ptr_a, lora
         int(lora_stride_b), _ptr(topk_ids), _ptr(topk_weights), _ptr(lora_ids), int(num_tokens), int(top_k),
         int(num_experts), int(rank), int(hidden_size), int(lora_dtype), float(scale), int(out_dtype), _ptr(out),
         _stream(stream)))
+    _written(out)
     return out
 
 
@@ -227,6 +240,7 @@ def nvfp4lora_moe_permute(x, num_tokens, row_bytes, topk_ids, top_k, num_experts
                                       int(padded_rows), _ptr(m_indptr), _ptr(expanded_idx_to_permuted_idx),
                                       _ptr(permuted_idx_to_expanded_idx), _ptr(workspace), int(workspace_bytes),
                                       _stream(stream)))
+    _written(rows, m_indptr, expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx, workspace)
     return rows
 
 
@@ -235,6 +249,7 @@ def nvfp4lora_moe_unpermute(y, padded_rows, H, dtype, expanded_idx_to_permuted_i
     _check(_lib.nvfp4lora_moe_unpermute(_ptr(y), int(padded_rows), int(H), int(dtype),
                                         _ptr(expanded_idx_to_permuted_idx), _ptr(topk_weights), int(num_tokens),
                                         int(top_k), _ptr(out), _stream(stream)))
+    _written(out)
     return out
 
 
@@ -243,6 +258,7 @@ def nvfp4lora_moe_permute_backward(grad_rows, padded_rows, H, dtype, expanded_id
     _check(_lib.nvfp4lora_moe_permute_backward(_ptr(grad_rows), int(padded_rows), int(H), int(dtype),
                                                _ptr(expanded_idx_to_permuted_idx), int(num_tokens), int(top_k),
                                                _ptr(grad_x), _stream(stream)))
+    _written(grad_x)
     return grad_x
 
 
@@ -253,12 +269,14 @@ def nvfp4lora_moe_unpermute_backward(grad_out, y, padded_rows, H, dtype, expande
         _ptr(grad_out), _ptr(y), int(padded_rows), int(H), int(dtype), _ptr(expanded_idx_to_permuted_idx),
         _ptr(permuted_idx_to_expanded_idx), _ptr(m_indptr), int(num_experts), _ptr(topk_weights), int(num_tokens),
         int(top_k), _ptr(grad_rows), _ptr(grad_weights), _stream(stream)))
+    _written(grad_rows, grad_weights)
     return grad_rows, grad_weights
 
 
 def nvfp4lora_fp8_quantize(x, rows, H, dtype, block_rows, q, scales, scale_stride_row, scale_stride_group, stream=None):
     _check(_lib.nvfp4lora_fp8_quantize(_ptr(x), int(rows), int(H), int(dtype), int(block_rows), _ptr(q), _ptr(scales),
                                        int(scale_stride_row), int(scale_stride_group), _stream(stream)))
+    _written(q, scales)
     return q, scales
 
 
@@ -267,6 +285,7 @@ def nvfp4lora_rmsnorm_fp8_quantize(x, residual, weight, rows, H, dtype, eps, nor
     _check(_lib.nvfp4lora_rmsnorm_fp8_quantize(_ptr(x), _ptr(residual), _ptr(weight), int(rows), int(H), int(dtype),
                                                float(eps), _ptr(norm_out), _ptr(q), _ptr(scales),
                                                int(scale_stride_row), int(scale_stride_group), _stream(stream)))
+    _written(residual, norm_out, q, scales)
     return q, scales
 
 
@@ -275,6 +294,7 @@ def nvfp4lora_mm_fp8(a, b, a_scale, a_scale_stride_m, a_scale_stride_k, b_scale,
     _check(_lib.nvfp4lora_mm_fp8(_ptr(a), _ptr(b), _ptr(a_scale), int(a_scale_stride_m), int(a_scale_stride_k),
                                  _ptr(b_scale), _ptr(bias), _ptr(out), int(out_dtype), int(M), int(N), int(K),
                                  _stream(stream)))
+    _written(out)
     return out
 
 
@@ -287,6 +307,7 @@ def nvfp4lora_device_status(stream=None) -> None:
 def nvfp4lora_quantize(x, rows, K, global_scale, codes, scales, stream=None):
     _check(_lib.nvfp4lora_quantize(_ptr(x), int(rows), int(K), _ptr(global_scale), _ptr(codes), _ptr(scales),
                                    scales.numel(), _stream(stream)))
+    _written(codes, scales)
     return codes, scales
 
 
@@ -765,13 +786,16 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
         _need_row_dtype(x, "x that requires gradients")
         _refuse_recording_in_capture("moe_permute", "moe_permute_backward")
         return MoePermutation(*_MoePermuteFn.apply(x, topk_ids, E, align, zero_padding, capacity))
+    given = out
     if out is None:
         out = x.new_empty((capacity, x.shape[1]))
     else:
         _need(out, "out", x.dtype, 2)
         if out.shape[0] < capacity or out.shape[1] != x.shape[1]:
             raise ValueError(f"out must be [capacity, H] with capacity >= {capacity} and H = {x.shape[1]}, got {tuple(out.shape)}")
-    return MoePermutation(*_moe_permute(x, topk_ids, E, align, zero_padding, out))
+    permutation = MoePermutation(*_moe_permute(x, topk_ids, E, align, zero_padding, out))
+    _written(given)
+    return permutation
 
 
 def moe_permute_backward(grad_rows: torch.Tensor, expanded_idx_to_permuted_idx: torch.Tensor, *,
@@ -785,6 +809,7 @@ def _moe_unpermute(y, idx, topk_weights, out, name="y"):
     _need_row_dtype(y, name)
     _need(y, name, y.dtype, 2)
     _need(idx, "expanded_idx_to_permuted_idx", torch.int32, 2)
+    given = out
     T, top_k = idx.shape
     H = y.shape[1]
     if topk_weights is not None:
@@ -800,6 +825,7 @@ def _moe_unpermute(y, idx, topk_weights, out, name="y"):
     _same_device(name, y, expanded_idx_to_permuted_idx=idx, topk_weights=topk_weights, out=out)
     _call(_lib.nvfp4lora_moe_unpermute, y.device, y.data_ptr(), y.shape[0], H, _ROW_DTYPES[y.dtype], idx.data_ptr(),
           None if topk_weights is None else topk_weights.data_ptr(), T, top_k, out.data_ptr())
+    _written(given)
     return out
 
 
@@ -866,6 +892,7 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
     _need(m_indptr, "m_indptr", torch.int32, 1)
     T, top_k = idx.shape
     rows, H = inv.shape[0], grad_out.shape[1]
+    given = grad_rows
     if grad_out.shape[0] != T:
         raise ValueError(f"grad_out has {grad_out.shape[0]} rows but expanded_idx_to_permuted_idx {T}")
     grad_weights = None
@@ -889,6 +916,7 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
           None if topk_weights is None else y.data_ptr(), rows, H, _ROW_DTYPES[grad_out.dtype], idx.data_ptr(),
           inv.data_ptr(), m_indptr.data_ptr(), m_indptr.shape[0] - 1, _ptr(topk_weights), T, top_k,
           grad_rows.data_ptr(), _ptr(grad_weights))
+    _written(given)
     return grad_rows, grad_weights
 
 
@@ -928,12 +956,14 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
     _need(x, "x", x.dtype, 2)
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows = {block_rows}: 1 or 128 is required")
+    given = q, scales
     q, scales = _fp8_outputs(x, block_rows, q, scales)
     _same_device("x", x, q=q, scales=scales)
     rows, H = x.shape
     sr, sg = scales.stride()
     _call(_lib.nvfp4lora_fp8_quantize, x.device, x.data_ptr(), rows, H, _ROW_DTYPES[x.dtype], block_rows, q.data_ptr(),
           scales.data_ptr(), sr, sg)
+    _written(*given)
     return q, scales
 
 
@@ -958,11 +988,13 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
             _need(t, name, x.dtype, 2)
             if t.shape != x.shape:
                 raise ValueError(f"{name} must be [rows, H] = {tuple(x.shape)}, got {tuple(t.shape)}")
+    given = residual, norm_out, q, scales
     q, scales = _fp8_outputs(x, 1, q, scales)
     _same_device("x", x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
     sr, sg = scales.stride()
     _call(_lib.nvfp4lora_rmsnorm_fp8_quantize, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), x.shape[0], H,
           _ROW_DTYPES[x.dtype], eps, _ptr(norm_out), q.data_ptr(), scales.data_ptr(), sr, sg)
+    _written(*given)
     return q, scales
 
 
@@ -997,6 +1029,7 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
             raise ValueError(f"bias must be [N] = [{N}]")
     if out_dtype not in _ROW_DTYPES:
         raise ValueError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
+    given = out
     if out is None:
         out = a.new_empty((M, N), dtype=out_dtype)
     else:
@@ -1007,4 +1040,5 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
     sm, sk = a_scale.stride()
     _call(_lib.nvfp4lora_mm_fp8, a.device, a.data_ptr(), b.data_ptr(), a_scale.data_ptr(), sm, sk, b_scale.data_ptr(),
           _ptr(bias), out.data_ptr(), _ROW_DTYPES[out_dtype], M, N, K)
+    _written(given)
     return out
