@@ -28,6 +28,7 @@ import os
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.graph import increment_version
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4lora.so")
@@ -732,6 +733,23 @@ def _refuse_gradient_in_capture(name: str) -> None:
                          f"{name}_backward inside the capture")
 
 
+def _refuse_gradients(name: str, **tensors) -> None:
+    """A call that records no graph refuses tensors that ask for one (None: not given): its results would lose their
+    gradients without an error.  Under torch.no_grad() nothing is asked for."""
+    if torch.is_grad_enabled():
+        for key, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} records no gradient and {key} requires one: detach it, or call under torch.no_grad()")
+    _refuse_tangents(name, **tensors)
+
+
+def _refuse_tangents(name: str, **tensors) -> None:
+    if forward_ad._current_level >= 0:             # inside a forward-mode context
+        for key, t in tensors.items():
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{name} has no forward-mode derivative and {key} carries a tangent")
+
+
 class _MoePermuteFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, topk_ids, num_experts, align, zero_padding, capacity):
@@ -764,7 +782,8 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
 
     Differentiable in x (bf16, fp16, fp32): the gradient is :func:`moe_permute_backward`; padding
     rows' gradients are not read.  Tensors that require gradients, and a recorded gradient's own pass, are
-    refused while a CUDA graph is captured (capture the two functions on detached tensors instead).  An id >= num_experts is read
+    refused while a CUDA graph is captured (capture the two functions on detached tensors instead), and so are
+    forward-mode tangents.  An id >= num_experts is read
     on the device: it counts as inactive and :func:`nvfp4lora_device_status` raises ValueError.
     """
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
@@ -780,6 +799,7 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
         raise ValueError(f"num_experts = {E}, align = {align}: 1 <= num_experts <= 1024 and 1 <= align <= 4096 are required")
     capacity = moe_capacity(T, top_k, E, align)
     _same_device("x", x, topk_ids=topk_ids, out=out)
+    _refuse_tangents("moe_permute", x=x)
     if x.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out is not supported for an x that requires gradients")
@@ -793,6 +813,7 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
         _need(out, "out", x.dtype, 2)
         if out.shape[0] < capacity or out.shape[1] != x.shape[1]:
             raise ValueError(f"out must be [capacity, H] with capacity >= {capacity} and H = {x.shape[1]}, got {tuple(out.shape)}")
+        _refuse_gradients("moe_permute into a given buffer", out=out)
     permutation = MoePermutation(*_moe_permute(x, topk_ids, E, align, zero_padding, out))
     _written(given)
     return permutation
@@ -801,7 +822,9 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
 def moe_permute_backward(grad_rows: torch.Tensor, expanded_idx_to_permuted_idx: torch.Tensor, *,
                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of :func:`moe_permute` by x: ``grad_x[t] = sum_j grad_rows[idx[t, j]]`` over the active
-    slots, in fp32 in slot order, rounded once."""
+    slots, in fp32 in slot order, rounded once.  Not differentiable itself."""
+    if isinstance(grad_rows, torch.Tensor):
+        _refuse_gradients("moe_permute_backward", grad_rows=grad_rows)
     return _moe_unpermute(grad_rows, expanded_idx_to_permuted_idx, None, out, "grad_rows")
 
 
@@ -822,6 +845,7 @@ def _moe_unpermute(y, idx, topk_weights, out, name="y"):
         _need(out, "out", y.dtype, 2)
         if out.shape != (T, H):
             raise ValueError(f"out must be [T, H] = [{T}, {H}], got {tuple(out.shape)}")
+        _refuse_gradients("a sum into a given buffer", out=out)
     _same_device(name, y, expanded_idx_to_permuted_idx=idx, topk_weights=topk_weights, out=out)
     _call(_lib.nvfp4lora_moe_unpermute, y.device, y.data_ptr(), y.shape[0], H, _ROW_DTYPES[y.dtype], idx.data_ptr(),
           None if topk_weights is None else topk_weights.data_ptr(), T, top_k, out.data_ptr())
@@ -859,8 +883,10 @@ def moe_unpermute(y: torch.Tensor, permutation, topk_weights: Optional[torch.Ten
 
     Differentiable in y and topk_weights where the whole MoePermutation is given (its gradient,
     :func:`moe_unpermute_backward`, needs the tables); as for :func:`moe_permute`, not while a CUDA
-    graph is captured.
+    graph is captured and not in forward mode.
     """
+    if isinstance(y, torch.Tensor):
+        _refuse_tangents("moe_unpermute", y=y, topk_weights=topk_weights)
     whole = isinstance(permutation, MoePermutation)
     idx = permutation.expanded_idx_to_permuted_idx if whole else permutation
     if torch.is_grad_enabled() and (getattr(y, "requires_grad", False) or getattr(topk_weights, "requires_grad", False)):
@@ -883,7 +909,8 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
     y[idx[t, j]]>`` (fp32; 0 for an inactive slot; None without weights, where y is not read and may be
     None).  Padding rows of the segments get zeros; rows from ``m_indptr[E]`` on are left as they were
     in ``grad_rows`` (a ``[rows, H]`` buffer, which may be y itself and must not overlap an input otherwise;
-    uninitialised there when None).  The tables are those of one :class:`MoePermutation`."""
+    uninitialised there when None).  The tables are those of one :class:`MoePermutation`.  Not differentiable
+    itself."""
     _need_row_dtype(grad_out, "grad_out")
     _need(grad_out, "grad_out", grad_out.dtype, 2)
     idx, inv = expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx
@@ -910,6 +937,8 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
         _need(grad_rows, "grad_rows", grad_out.dtype, 2)
         if grad_rows.shape != (rows, H):
             raise ValueError(f"grad_rows must be [rows, H] = [{rows}, {H}], got {tuple(grad_rows.shape)}")
+    _refuse_gradients("moe_unpermute_backward", grad_out=grad_out, grad_rows=given)
+    _refuse_tangents("moe_unpermute_backward", y=y, topk_weights=topk_weights)
     _same_device("grad_out", grad_out, y=y, expanded_idx_to_permuted_idx=idx, permuted_idx_to_expanded_idx=inv,
                  m_indptr=m_indptr, topk_weights=topk_weights, grad_rows=grad_rows)
     _call(_lib.nvfp4lora_moe_unpermute_backward, grad_out.device, grad_out.data_ptr(),
@@ -951,7 +980,8 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
     (activations; scales are column-major unless given).  ``block_rows=128``: a scale per 128 x 128
     block (weights).  Rule, in fp32: ``amax = max(max |x|, 2^-100)``, ``scale = amax / 448``,
     ``q = e4m3(x * (448 / amax))``, nearest even.  Finite values are expected: a NaN stays a NaN, an
-    infinity makes its group's scale infinite.  q and scales must not overlap x or each other.  Not differentiable."""
+    infinity makes its group's scale infinite.  q and scales must not overlap x or each other.  Not differentiable: a tensor
+    that requires gradients is refused outside ``torch.no_grad()``."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)
     if block_rows not in (1, 128):
@@ -959,6 +989,7 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
     given = q, scales
     q, scales = _fp8_outputs(x, block_rows, q, scales)
     _same_device("x", x, q=q, scales=scales)
+    _refuse_gradients("fp8_quantize", x=x, q=q, scales=scales)
     rows, H = x.shape
     sr, sg = scales.stride()
     _call(_lib.nvfp4lora_fp8_quantize, x.device, x.data_ptr(), rows, H, _ROW_DTYPES[x.dtype], block_rows, q.data_ptr(),
@@ -976,7 +1007,8 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
     with ``block_rows=1`` gives them (from the unrounded y), the ``a`` and ``a_scale`` of
     :func:`mm_fp8`.  ``norm_out [rows, H]`` also receives y in x's type (a router or a LoRA down
     projection reads it); x may be norm_out or residual itself, and no other result overlaps another buffer of
-    the call.  x, weight ``[H]``, residual and norm_out share one type (bf16, fp16 or fp32).  Not differentiable."""
+    the call.  x, weight ``[H]``, residual and norm_out share one type (bf16, fp16 or fp32).  Not differentiable: a tensor that
+    requires gradients is refused outside ``torch.no_grad()``."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)
     H = x.shape[1]
@@ -991,6 +1023,7 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
     given = residual, norm_out, q, scales
     q, scales = _fp8_outputs(x, 1, q, scales)
     _same_device("x", x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
+    _refuse_gradients("add_rmsnorm_fp8_quantize", x=x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
     sr, sg = scales.stride()
     _call(_lib.nvfp4lora_rmsnorm_fp8_quantize, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), x.shape[0], H,
           _ROW_DTYPES[x.dtype], eps, _ptr(norm_out), q.data_ptr(), scales.data_ptr(), sr, sg)
@@ -1008,7 +1041,8 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
     strides (column-major, as :func:`fp8_quantize` makes it, is read fastest); b_scale: fp32
     ``[ceil(N / 128), ceil(K / 128)]`` contiguous; bias: bf16 ``[N]``; out overlaps none of them.  K % 16 == 0; any M, N >= 1.  As for
     :func:`mm_nvfp4_lora`, out is defined once a later :func:`nvfp4lora_device_status` has returned
-    without raising ``DeviceTimeoutError``.  Not differentiable."""
+    without raising ``DeviceTimeoutError``.  Not differentiable: a tensor that requires gradients is refused
+    outside ``torch.no_grad()``."""
     _need(a, "a", torch.float8_e4m3fn, 2)
     _need(b, "b", torch.float8_e4m3fn, 2)
     _need(b_scale, "b_scale", torch.float32, 2)
@@ -1037,6 +1071,7 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
         if out.shape != (M, N):
             raise ValueError(f"out must be [M, N] = [{M}, {N}]")
     _same_device("a", a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
+    _refuse_gradients("mm_fp8", a=a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
     sm, sk = a_scale.stride()
     _call(_lib.nvfp4lora_mm_fp8, a.device, a.data_ptr(), b.data_ptr(), a_scale.data_ptr(), sm, sk, b_scale.data_ptr(),
           _ptr(bias), out.data_ptr(), _ROW_DTYPES[out_dtype], M, N, K)
