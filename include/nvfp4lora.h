@@ -208,6 +208,7 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_grouped_mm(
  * whose bounded wait gives up returns early and leaves its outputs (out, b_folded, ratio, codes,
  * scales) partly unwritten.  Their contents are therefore defined only once a later
  * nvfp4lora_device_status on the same stream has returned NVFP4LORA_OK.
+ * One code is kept between two calls: a time-out before any other, else the first that was reported.
  */
 NVFP4LORA_API nvfp4lora_status nvfp4lora_device_status(nvfp4lora_stream stream);
 

@@ -187,7 +187,7 @@ bgmv_delta_kernel(const BgmvArgs args) {
                 // this CTA's B rows [h0, h1) are contiguous: pull them into L2 for the expand
                 if (h1 > h0) bulk_prefetch_l2(s.b + (int64_t)h0 * (rank / 8), (uint32_t)((h1 - h0) * rank * 2));
             } else {
-                atomicExch(&g_device_error, kErrBadRoute);
+                report_bad_entry(kErrBadRoute);
             }
         }
         slots[tid] = s;

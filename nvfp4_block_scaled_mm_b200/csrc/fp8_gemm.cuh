@@ -110,7 +110,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, 
         if (abort != nullptr && *abort) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             if (abort != nullptr) *abort = 1;
-            atomicExch(&g_device_error, kErrTimeout);
+            report_timeout();
             return false;
         }
     }

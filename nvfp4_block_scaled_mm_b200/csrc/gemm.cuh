@@ -464,7 +464,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
             __syncwarp();
             if (lane == 0) {
                 ind[kMaxExperts + 1] = valid ? ind[E] / kTileM : 0;
-                if (!valid) atomicExch(&g_device_error, kErrBadIndptr);
+                if (!valid) report_bad_entry(kErrBadIndptr);
                 mbar_arrive(groups_ready);
             }
         }

@@ -151,7 +151,7 @@ moe_permute_kernel(const PermuteArgs a) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (e[q] >= 0 && e[q] < E) atomicAdd(i0 + q * NT + tid < start ? &before[e[q]] : &total[e[q]], 1);
-                else if (e[q] >= E && blockIdx.x == 0) atomicExch(&g_device_error, kErrBadSlot);
+                else if (e[q] >= E && blockIdx.x == 0) report_bad_entry(kErrBadSlot);
             }
         }
         __syncthreads();
@@ -191,7 +191,7 @@ moe_permute_kernel(const PermuteArgs a) {
             const bool in = s + lane < ns;
             int e = in ? a.ids[i] : -1;
             if (e >= E) {
-                if (a.counts != nullptr) atomicExch(&g_device_error, kErrBadSlot);
+                if (a.counts != nullptr) report_bad_entry(kErrBadSlot);
                 e = -1;
             }
             const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
@@ -385,7 +385,7 @@ moe_unpermute_kernel(const UnpermuteArgs a) {
         my_row = a.idx[t * k + lane];
         if (a.w != nullptr) my_w = a.w[t * k + lane];
         if (my_row >= a.rows) {
-            atomicExch(&g_device_error, kErrBadSlot);
+            report_bad_entry(kErrBadSlot);
             my_row = -1;
         }
     }
@@ -471,7 +471,7 @@ moe_unpermute_bwd_kernel(const UnpermuteBwdArgs a) {
             r[j] = j0 + j < k ? a.idx[t * k + j0 + j] : -1;
             w[j] = j0 + j < k && a.w != nullptr ? a.w[t * k + j0 + j] : 1.0f;
             if (r[j] >= a.rows) {
-                if (tid == 0) atomicExch(&g_device_error, kErrBadSlot);
+                if (tid == 0) report_bad_entry(kErrBadSlot);
                 r[j] = -1;
             }
         }

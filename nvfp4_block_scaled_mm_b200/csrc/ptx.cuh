@@ -12,12 +12,18 @@ namespace nvfp4lora {
 // error word and bounded waits
 // ------------------------------------------------------------------------------------
 
-// Set (to a non-zero code) by any kernel whose bounded wait runs out.  Read and
-// cleared by nvfp4lora_device_status on the host.  Defined here: the library is built
-// as a single translation unit (abi.cu), which includes this header once.
+// Set (to a non-zero code) by any kernel whose bounded wait runs out, or that finds an entry
+// of a table on the device out of range.  Read and cleared by nvfp4lora_device_status on the
+// host.  Defined here: the library is built as a single translation unit (abi.cu), which
+// includes this header once.
 __device__ int g_device_error = 0;
 
 constexpr int kErrTimeout = 1;
+
+// A time-out replaces any other code and is replaced by none: results are undefined from it on,
+// while a bad entry is left out and the rest computed.
+__device__ __forceinline__ void report_timeout() { atomicExch(&g_device_error, kErrTimeout); }
+__device__ __forceinline__ void report_bad_entry(int code) { atomicCAS(&g_device_error, 0, code); }
 // A wait that has not completed after this long is treated as a pipeline failure.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
@@ -79,7 +85,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
         if (abort != nullptr && *abort) return false;
         if (global_timer_ns() - t0 > limit_ns) {
             if (abort != nullptr) *abort = 1;
-            atomicExch(&g_device_error, kErrTimeout);
+            report_timeout();
             return false;
         }
     }
@@ -310,7 +316,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
         if (abort != nullptr && *abort) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             if (abort != nullptr) *abort = 1;
-            atomicExch(&g_device_error, kErrTimeout);
+            report_timeout();
             return false;
         }
     }
