@@ -163,6 +163,16 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _launch(fn, anchor: torch.Tensor, stream, *args) -> None:
+    """Run a C entry point on `stream`, or on the current stream of the anchor tensor's device, with the stream's
+    device current (the library launches on the current device)."""
+    if stream is None:
+        _call(fn, anchor.device, *args)
+    else:
+        with torch.cuda.device(stream.device):
+            _check(fn(*args, stream.cuda_stream))
+
+
 def _written(*tensors) -> None:
     """Count a write by address in the version counters of the caller's buffers (None: not given), as an in-place
     operation of torch does: autograd then refuses to use a saved tensor that a call has overwritten."""
@@ -236,29 +246,26 @@ def nvfp4lora_bgmv_moe_gemm2_lora_delta(act, padded_rows, I, perm, w_ptr_a, lora
 def nvfp4lora_moe_permute(x, num_tokens, row_bytes, topk_ids, top_k, num_experts, align, zero_padding, rows,
                           padded_rows, m_indptr, expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx,
                           workspace=None, workspace_bytes=0, stream=None):
-    _check(_lib.nvfp4lora_moe_permute(_ptr(x), int(num_tokens), int(row_bytes), _ptr(topk_ids), int(top_k),
-                                      int(num_experts), int(align), int(bool(zero_padding)), _ptr(rows),
-                                      int(padded_rows), _ptr(m_indptr), _ptr(expanded_idx_to_permuted_idx),
-                                      _ptr(permuted_idx_to_expanded_idx), _ptr(workspace), int(workspace_bytes),
-                                      _stream(stream)))
+    _launch(_lib.nvfp4lora_moe_permute, m_indptr, stream, _ptr(x), int(num_tokens), int(row_bytes), _ptr(topk_ids),
+            int(top_k), int(num_experts), int(align), int(bool(zero_padding)), _ptr(rows), int(padded_rows),
+            _ptr(m_indptr), _ptr(expanded_idx_to_permuted_idx), _ptr(permuted_idx_to_expanded_idx), _ptr(workspace),
+            int(workspace_bytes))
     _written(rows, m_indptr, expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx, workspace)
     return rows
 
 
 def nvfp4lora_moe_unpermute(y, padded_rows, H, dtype, expanded_idx_to_permuted_idx, topk_weights, num_tokens, top_k,
                             out, stream=None):
-    _check(_lib.nvfp4lora_moe_unpermute(_ptr(y), int(padded_rows), int(H), int(dtype),
-                                        _ptr(expanded_idx_to_permuted_idx), _ptr(topk_weights), int(num_tokens),
-                                        int(top_k), _ptr(out), _stream(stream)))
+    _launch(_lib.nvfp4lora_moe_unpermute, out, stream, _ptr(y), int(padded_rows), int(H), int(dtype),
+            _ptr(expanded_idx_to_permuted_idx), _ptr(topk_weights), int(num_tokens), int(top_k), _ptr(out))
     _written(out)
     return out
 
 
 def nvfp4lora_moe_permute_backward(grad_rows, padded_rows, H, dtype, expanded_idx_to_permuted_idx, num_tokens, top_k,
                                    grad_x, stream=None):
-    _check(_lib.nvfp4lora_moe_permute_backward(_ptr(grad_rows), int(padded_rows), int(H), int(dtype),
-                                               _ptr(expanded_idx_to_permuted_idx), int(num_tokens), int(top_k),
-                                               _ptr(grad_x), _stream(stream)))
+    _launch(_lib.nvfp4lora_moe_permute_backward, grad_x, stream, _ptr(grad_rows), int(padded_rows), int(H), int(dtype),
+            _ptr(expanded_idx_to_permuted_idx), int(num_tokens), int(top_k), _ptr(grad_x))
     _written(grad_x)
     return grad_x
 
@@ -266,35 +273,33 @@ def nvfp4lora_moe_permute_backward(grad_rows, padded_rows, H, dtype, expanded_id
 def nvfp4lora_moe_unpermute_backward(grad_out, y, padded_rows, H, dtype, expanded_idx_to_permuted_idx,
                                      permuted_idx_to_expanded_idx, m_indptr, num_experts, topk_weights, num_tokens,
                                      top_k, grad_rows, grad_weights, stream=None):
-    _check(_lib.nvfp4lora_moe_unpermute_backward(
-        _ptr(grad_out), _ptr(y), int(padded_rows), int(H), int(dtype), _ptr(expanded_idx_to_permuted_idx),
-        _ptr(permuted_idx_to_expanded_idx), _ptr(m_indptr), int(num_experts), _ptr(topk_weights), int(num_tokens),
-        int(top_k), _ptr(grad_rows), _ptr(grad_weights), _stream(stream)))
+    _launch(_lib.nvfp4lora_moe_unpermute_backward, m_indptr, stream, _ptr(grad_out), _ptr(y), int(padded_rows), int(H),
+            int(dtype), _ptr(expanded_idx_to_permuted_idx), _ptr(permuted_idx_to_expanded_idx), _ptr(m_indptr),
+            int(num_experts), _ptr(topk_weights), int(num_tokens), int(top_k), _ptr(grad_rows), _ptr(grad_weights))
     _written(grad_rows, grad_weights)
     return grad_rows, grad_weights
 
 
 def nvfp4lora_fp8_quantize(x, rows, H, dtype, block_rows, q, scales, scale_stride_row, scale_stride_group, stream=None):
-    _check(_lib.nvfp4lora_fp8_quantize(_ptr(x), int(rows), int(H), int(dtype), int(block_rows), _ptr(q), _ptr(scales),
-                                       int(scale_stride_row), int(scale_stride_group), _stream(stream)))
+    _launch(_lib.nvfp4lora_fp8_quantize, q, stream, _ptr(x), int(rows), int(H), int(dtype), int(block_rows), _ptr(q),
+            _ptr(scales), int(scale_stride_row), int(scale_stride_group))
     _written(q, scales)
     return q, scales
 
 
 def nvfp4lora_rmsnorm_fp8_quantize(x, residual, weight, rows, H, dtype, eps, norm_out, q, scales, scale_stride_row,
                                    scale_stride_group, stream=None):
-    _check(_lib.nvfp4lora_rmsnorm_fp8_quantize(_ptr(x), _ptr(residual), _ptr(weight), int(rows), int(H), int(dtype),
-                                               float(eps), _ptr(norm_out), _ptr(q), _ptr(scales),
-                                               int(scale_stride_row), int(scale_stride_group), _stream(stream)))
+    _launch(_lib.nvfp4lora_rmsnorm_fp8_quantize, q, stream, _ptr(x), _ptr(residual), _ptr(weight), int(rows), int(H),
+            int(dtype), float(eps), _ptr(norm_out), _ptr(q), _ptr(scales), int(scale_stride_row),
+            int(scale_stride_group))
     _written(residual, norm_out, q, scales)
     return q, scales
 
 
 def nvfp4lora_mm_fp8(a, b, a_scale, a_scale_stride_m, a_scale_stride_k, b_scale, bias, out, out_dtype, M, N, K,
                      stream=None):
-    _check(_lib.nvfp4lora_mm_fp8(_ptr(a), _ptr(b), _ptr(a_scale), int(a_scale_stride_m), int(a_scale_stride_k),
-                                 _ptr(b_scale), _ptr(bias), _ptr(out), int(out_dtype), int(M), int(N), int(K),
-                                 _stream(stream)))
+    _launch(_lib.nvfp4lora_mm_fp8, out, stream, _ptr(a), _ptr(b), _ptr(a_scale), int(a_scale_stride_m),
+            int(a_scale_stride_k), _ptr(b_scale), _ptr(bias), _ptr(out), int(out_dtype), int(M), int(N), int(K))
     _written(out)
     return out
 
