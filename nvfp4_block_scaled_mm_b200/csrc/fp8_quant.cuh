@@ -140,7 +140,7 @@ constexpr int kNormShortRows = 8;          // rows (warps) of a SHORT CTA
 template <MoeType TY, int NV, bool VEC, bool SHORT>
 __global__ void __launch_bounds__(kNormMaxThreads, SHORT || !VEC ? 0 : NV == 4 ? 2 : NV == 1 && TY != MoeType::FP32 ? 4 : 0)
 rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
-    using C = RowChunk<TY, VEC>;
+    using C = RowChunk<TY, VEC, VEC>;          // with VEC, H % 8 == 0
     __shared__ float red[32];
     const int lane = threadIdx.x & 31, warp = SHORT ? 0 : threadIdx.x >> 5, nw = SHORT ? 1 : blockDim.x >> 5;
     const int64_t row = SHORT ? (int64_t)blockIdx.x * kNormShortRows + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
@@ -318,7 +318,7 @@ row_fp8_kernel(const Fp8QuantArgs a) {
 template <MoeType TY, bool BLOCK>
 __global__ void __launch_bounds__(256)
 quantize_fp8_tile_kernel(const Fp8QuantArgs a) {
-    using R = RowChunk<TY, true>;
+    using R = RowChunk<TY, true, true>;
     __shared__ float red[8];
     const int nv = (int)(a.H / 8);
     const int64_t gcols = (a.H + 127) / 128;

@@ -280,9 +280,10 @@ __device__ __forceinline__ typename MoeElem<TY>::type from_f32(float f) {   // n
 
 // A warp's share of a row: 256 elements from element e0 on, eight per lane.  VEC: the lane's eight are
 // neighbours, one 16-byte access (two for fp32, each bounded by itself: a row of 12 ends between a lane's two);
-// rows are whole numbers of 16 bytes long and start on 16-byte boundaries.  Otherwise they are 32 apart, so that
-// any alignment is read and written in coalesced element accesses.
-template <MoeType TY, bool VEC>
+// rows are whole numbers of 16 bytes long and start on 16-byte boundaries.  EIGHT: the length is a multiple of 8, and
+// one bound serves a lane (the norm of 4096 x 12288 fp32, where the second one spills: 115 us, 123 with it).  Without
+// VEC they are 32 apart, so that any alignment is read and written in coalesced element accesses.
+template <MoeType TY, bool VEC, bool EIGHT = false>
 struct RowChunk {
     using E = typename MoeElem<TY>::type;
     static constexpr int NW = 8 * (int)sizeof(E) / 16;
@@ -297,7 +298,15 @@ struct RowChunk {
     static __device__ __forceinline__ Raw load(const void* row, int64_t e0, int64_t H, int lane) {
         Raw r;
         const E* p = static_cast<const E*>(row);
-        if constexpr (VEC) {
+        if constexpr (VEC && EIGHT) {
+            if (at(e0, lane, 0) < H) {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) r.w[i] = reinterpret_cast<const uint4*>(p + at(e0, lane, 0))[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
+            }
+        } else if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < NW; ++i)
                 r.w[i] = at(e0, lane, i * PER) < H ? reinterpret_cast<const uint4*>(p + at(e0, lane, 0))[i] : make_uint4(0, 0, 0, 0);
@@ -333,7 +342,12 @@ struct RowChunk {
                 u[i] = (uint32_t)from_f32<TY>(f[2 * i]) | ((uint32_t)from_f32<TY>(f[2 * i + 1]) << 16);
             r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        if constexpr (VEC) {
+        if constexpr (VEC && EIGHT) {
+            if (at(e0, lane, 0) < H) {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) reinterpret_cast<uint4*>(p + at(e0, lane, 0))[i] = r.w[i];
+            }
+        } else if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < NW; ++i)
                 if (at(e0, lane, i * PER) < H) reinterpret_cast<uint4*>(p + at(e0, lane, 0))[i] = r.w[i];
