@@ -244,6 +244,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
     uint64_t* drain = acc_empty + L::PRODUCTS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+    volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(smem + L::MISC_OFF + 8);   // K blocks copied by this CTA
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -286,7 +287,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
             // ------------------------------- TMA producer (both CTAs) -------------------------------
             grid_dependency_wait();
             int stage = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, n = 0;
             bool ok = true;
             for (int tile = pair; ok && tile < args.num_tiles; tile += npairs) {
                 int m_blk, n_blk;
@@ -294,7 +295,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                 const int row_a = m_blk * kFp8TileM + (int)rank * 128;   // this CTA's A rows
                 const int row_b = n_blk * TN + (int)rank * (TN / 2);   // and B half
                 int kx = fp8_first_block(m_blk, n_blk, args.kblocks);
-                for (int kb = 0; kb < args.kblocks; ++kb) {
+                for (int kb = 0; kb < args.kblocks; ++kb, ++n) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
                     const uint32_t lead_full = map_to_rank(smem_u32(&full[stage]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE_TX);
@@ -304,6 +305,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
                     if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
                 }
             }
+            *issued = n;
         } else if (warp == 1 && rank == 0) {
             // ------------------------------- MMA issuer (the leader) -------------------------------
             grid_dependency_wait();
@@ -455,12 +457,8 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_cons
         if (args.out_bytes == 16 && lane == 0) bulk_wait_group_all();
     }
 
-    // Neither CTA leaves (or gives TMEM back) while the other may still reach its barriers or the
-    // leader's MMAs its TMEM: the whole pair meets here first.
     tc_fence_before();
-    __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+    pair_finish(full, L::STAGES, issued, abort_flag);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);

@@ -91,6 +91,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// After a wait has run out, before the CTA's shared memory is given up: wait for the copies of the last items of a
+// ring.  Item k uses stage k % stages and completes the phase of parity (k / stages) & 1 of that stage's barrier; n
+// items have been issued, and those before the last `stages` had been consumed.  One limit for all of them: an item
+// whose other half was never issued does not complete, and by then its copies have landed.
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t stages, uint32_t n,
+                                           unsigned long long limit_ns = kWaitLimitNs) {
+    const unsigned long long t0 = global_timer_ns();
+    for (uint32_t k = n > stages ? n - stages : 0; k < n; ++k)
+        while (!mbar_try_wait(&full[k % stages], (k / stages) & 1u))
+            if (global_timer_ns() - t0 > limit_ns) return;
+}
+
 // ------------------------------------------------------------------------------------
 // TMA and bulk copies (global -> shared, completion counted on an mbarrier)
 // ------------------------------------------------------------------------------------
@@ -376,6 +388,17 @@ __device__ __forceinline__ void st_async_v4(uint32_t caddr, float a, float b, fl
                  ::"r"(caddr), "f"(a), "f"(b), "f"(c), "f"(d), "r"(cbar) : "memory");
 }
 
+// A word of another CTA's shared memory (cluster address from map_to_rank).  Ordered by the cluster barrier.
+__device__ __forceinline__ void st_cluster_u32(uint32_t caddr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
+    return v;
+}
+
 // Split cluster barrier: every thread of every CTA arrives once, early; a thread that is about
 // to touch another CTA's shared memory waits first.
 __device__ __forceinline__ void cluster_arrive() {
@@ -496,6 +519,25 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         " [%0], [%1, {%3, %4}], [%2];"
         ::"r"(smem_u32(dst)), "l"(map), "r"(leader_bar), "r"(x), "r"(y)
         : "memory");
+}
+
+// The end of a pair kernel, by all threads of both CTAs, once a CTA's warps are done: neither CTA leaves (or gives TMEM
+// back) while the other may still reach its barriers or the leader's MMAs its TMEM.  If a wait of either has run out, the
+// leader, on whose barriers both CTAs' copies complete, waits for what either has issued (`issued`: the ring items of
+// this CTA's producer) before the pair gives up its shared memory.
+__device__ __forceinline__ void pair_finish(uint64_t* full, uint32_t stages, volatile uint32_t* issued, volatile int* abort) {
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort) st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(abort)), cluster_rank() ^ 1u), 1u);
+    cluster_arrive();
+    cluster_wait();
+    if (*abort) {
+        if (threadIdx.x == 0 && cluster_rank() == 0) {
+            const uint32_t other = ld_cluster_u32(map_to_rank(smem_u32(const_cast<uint32_t*>(issued)), 1u));
+            drain_ring(full, stages, max(*issued, other));
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 }  // namespace nvfp4lora
