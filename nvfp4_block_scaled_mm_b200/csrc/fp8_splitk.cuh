@@ -110,6 +110,7 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     uint64_t* drain = acc_empty + L::NB;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+    volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(smem + L::MISC_OFF + 8);   // K blocks copied
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -166,20 +167,15 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int kb = k0 + L::STAGES; kb < k1; ++kb) {
-                if (!mbar_wait_short(&empty[stage], phase, abort_flag)) { ok = false; break; }
+            int kb = k0 + L::STAGES;
+            for (; kb < k1; ++kb) {
+                if (!mbar_wait_short(&empty[stage], phase, abort_flag)) break;
                 mbar_arrive_expect_tx(&full[stage], L::W_BYTES + L::X_BYTES);
                 tma_load_2d(smem + L::W_OFF + stage * L::W_BYTES, &tm_b, &full[stage], kb * 128, n_blk * 128);
                 tma_load_2d(smem + L::X_OFF + stage * L::X_BYTES, &tm_a, &full[stage], kb * 128, m0);
                 if (++stage == L::STAGES) { stage = 0; phase ^= 1; }
             }
-            if (!ok || *abort_flag) {
-                // Let the copies already issued land before the CTA can exit: the stages before `stage` were
-                // filled in this round too, with the other parity.
-                for (int s = 0; s < L::STAGES; ++s)
-                    if (k0 + s < k1) mbar_wait(&full[s], s < stage ? phase ^ 1 : phase, nullptr);
-            }
+            *issued = (uint32_t)(min(kb, k1) - k0);
         }
         __syncwarp();
     } else if (warp <= kSplitIssuers) {
@@ -350,6 +346,8 @@ fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constan
     // every read of the accumulators lies before this point
     tc_fence_before();
     __syncthreads();
+    // whichever warp's wait ran out: the copies already issued land before the CTA can exit
+    if (threadIdx.x == 0 && *abort_flag) drain_ring(full, L::STAGES, *issued);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, L::TMEM_COLS);
