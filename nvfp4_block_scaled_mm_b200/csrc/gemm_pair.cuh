@@ -152,6 +152,7 @@ nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     uint64_t* bias_empty = bias_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+    volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(smem + L::MISC_OFF + 8);   // ring items of this CTA
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -216,7 +217,7 @@ nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             const bool lora_on = (MODE != Mode::Off) && sv != 0.0f;
             const bool bias_smem = args.bias != nullptr && args.vec_out;
             int stage = 0, tl = 0;
-            uint32_t phase = 0, bias_issued = 0, bias_par = 0;
+            uint32_t phase = 0, items = 0, bias_issued = 0, bias_par = 0;
             bool ok = true;
             bool pend = false;                 // raw: the previous tile's LoRA half 1 is still due
             int prev_m = 0, prev_n = 0;
@@ -227,6 +228,7 @@ nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                 sa = smem + L::A_OFF + stage * L::A_BYTES;
                 sb = smem + L::B_OFF + stage * L::B_BYTES;
                 if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * tx);
+                ++items;
                 if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 return true;
             };
@@ -294,10 +296,10 @@ nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             }
             if (ok && MODE == Mode::Raw && pend)
                 for (int c = 0; ok && c < lora_chunks_if_on; ++c) ok = emit_half(c, 1, prev_m, prev_n);
+            *issued = items;
             if (!ok || *abort_flag) {
                 // Let this CTA's own-barrier copies land before it can exit (the pair's code-tile
-                // loads complete on the leader's barriers; both CTAs meet at the final cluster
-                // barrier).
+                // loads complete on the leader's barriers, which pair_finish waits for).
                 for (int k = 0; k < 2; ++k)
                     if ((bias_issued >> k) & 1u) mbar_wait(&bias_full[k], (bias_par >> k) & 1u, nullptr);
             }
@@ -609,12 +611,8 @@ nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         if (args.vec_out && lane == 0) bulk_wait_group_all();
     }
 
-    // Neither CTA leaves (or gives TMEM back) while the other may still reach its barriers or the
-    // leader's MMAs its TMEM: the whole pair meets here first.
     tc_fence_before();
-    __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+    pair_finish(full, STAGES, issued, abort_flag);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, T::ALLOC);
