@@ -368,7 +368,8 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_unpermute_backward(
  *     amax = max(max |x|, 2^-100);  scale = amax / 448;  q = E4M3(rne)(x * (448 / amax)),
  * so value(q) * scale approximates x.  The last group of a row, and the last block, may be partial.
  *   x       [rows, H] of `dtype` (bf16, fp16 or fp32), contiguous, aligned to its elements.
- *           Finite values: a NaN stays a NaN and an infinity makes its group's scale infinite.
+ *           Finite values: a NaN stays a NaN; an infinity makes its group's scale infinite, itself a NaN and
+ *           the group's finite values zeros.
  *   q       uint8 [rows, H]: E4M3 bytes.
  *   scales  fp32 [ceil(rows / block_rows), ceil(H / 128)], element (r, g) at
  *           r * scale_stride_row + g * scale_stride_group (row-major or column-major, no overlap).
@@ -385,6 +386,7 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_fp8_quantize(
  *     h = x + residual;  residual <- round(h) (in place);
  *     y = h * (1 / sqrt(mean(h^2) + eps)) * weight;  norm_out <- round(y);
  *     (q, scales) as nvfp4lora_fp8_quantize with block_rows = 1 gives them for the unrounded y.
+ * A row whose mean square passes fp32's range (an infinity, values of about 1e19) gives zeros, and NaN for its infinities.
  * residual NULL: h = x, nothing is written back.  norm_out NULL: not written.  x, residual, weight [H]
  * and norm_out have one type `dtype`; x may be the buffer of norm_out or of residual.  No other two of x,
  * residual, weight, norm_out, q and the scales' elements share bytes, but x and weight, which are only read.

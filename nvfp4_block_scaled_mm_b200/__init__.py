@@ -985,7 +985,7 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
     (activations; scales are column-major unless given).  ``block_rows=128``: a scale per 128 x 128
     block (weights).  Rule, in fp32: ``amax = max(max |x|, 2^-100)``, ``scale = amax / 448``,
     ``q = e4m3(x * (448 / amax))``, nearest even.  Finite values are expected: a NaN stays a NaN, an
-    infinity makes its group's scale infinite.  q and scales must not overlap x or each other.  Not differentiable: a tensor
+    infinity makes its group's scale infinite, itself a NaN and the group's finite values zeros.  q and scales must not overlap x or each other.  Not differentiable: a tensor
     that requires gradients is refused outside ``torch.no_grad()``."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)
@@ -1012,7 +1012,8 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
     with ``block_rows=1`` gives them (from the unrounded y), the ``a`` and ``a_scale`` of
     :func:`mm_fp8`.  ``norm_out [rows, H]`` also receives y in x's type (a router or a LoRA down
     projection reads it); x may be norm_out or residual itself, and no other result overlaps another buffer of
-    the call.  x, weight ``[H]``, residual and norm_out share one type (bf16, fp16 or fp32).  Not differentiable: a tensor that
+    the call.  A row whose mean square passes fp32's range (an infinity, values of about 1e19) gives zeros, and
+    NaN for its infinities.  x, weight ``[H]``, residual and norm_out share one type (bf16, fp16 or fp32).  Not differentiable: a tensor that
     requires gradients is refused outside ``torch.no_grad()``."""
     _need_row_dtype(x, "x")
     _need(x, "x", x.dtype, 2)

@@ -8,7 +8,9 @@
 //     h = x + residual;   residual <- round(h);   y = h * (1 / sqrt(mean(h^2) + eps)) * weight,
 // all in fp32: the sum of squares, y and the group maxima come from the unrounded h, so that q is
 // the only rounding to fewer bits on its path.
-// A NaN stays a NaN in q and is ignored by amax; an infinity makes its group's scale infinite.
+// A NaN stays a NaN in q and is ignored by amax; an infinity makes its group's scale infinite, itself a NaN and
+// the group's finite values zeros.  In the norm an infinity, or finite values whose mean square passes fp32's range,
+// make rms zero: zeros, and a NaN in an infinity's place.
 //
 // HBM-bound: the norm of 8192 x 8192 bf16 with residual and the normed rows kept runs 92 us (6.6 TB/s), of 65536 x 512
 // 36 us (6.5); without either, where it moves 3 bytes per element, it is bound by instruction issue (46 us, 4.4).

@@ -350,3 +350,66 @@ def test_fp32_rows_of_four_modulo_eight(T, H):
     _, ref = R.add_rmsnorm(f64(x), f64(r), f64(w), 1e-5)
     rel = (H / 256 + 42) / 2 * 2.0 ** -24 + 12 * 2.0 ** -24
     assert np.all(np.abs(f64(out) - ref) <= (2.0 ** -24 + rel) * np.abs(ref) + torch.finfo(FP).tiny)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("H", [512, 510])            # registers of aligned rows, and elements
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+def test_quantizer_infinities(dt, H, block_rows):
+    """An infinity makes its group's scale infinite: it becomes a NaN and the group's finite values zeros of their sign;
+    a NaN stays one, and other groups are as without it."""
+    import nvfp4_block_scaled_mm_b200 as L
+    x = randn(256, H, dtype=dt, seed=4)
+    clean = x.clone()
+    x[3, 130], x[3, 140], x[3, 200] = float("inf"), float("nan"), -0.0
+    x[200, 300], x[200, 301] = float("-inf"), float("inf")
+    q, s = L.fp8_quantize(x.to(DEV), block_rows=block_rows)
+    wq, ws = R.fp8_quantize(clean.float().numpy(), block_rows)
+    got_q, got_s = codes(q), s.cpu().numpy()
+    hit = np.zeros(ws.shape, dtype=bool)
+    hit[3 // block_rows, 1] = hit[200 // block_rows, 2] = True
+    cells = np.repeat(np.repeat(hit, block_rows, axis=0), 128, axis=1)[:256, :H]
+    assert np.all(np.isposinf(got_s[hit])) and np.array_equal(got_s[~hit], ws[~hit])
+    assert np.array_equal(got_q[~cells], wq[~cells])
+    bad = (~torch.isfinite(x)).numpy()
+    assert np.all((got_q[bad] & 0x7F) == 0x7F)
+    finite = cells & ~bad
+    sign = np.signbit(x.float().numpy())
+    assert np.array_equal(got_q[finite], np.where(sign[finite], 0x80, 0))
+
+
+@pytest.mark.parametrize("T,H", [(6, 512), (1200, 256), (6, 1000), (6, 1001), (1200, 4104), (6, 16392), (6, 16385)])
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+def test_norm_infinities(T, H, dt):
+    """An infinity in x + residual makes the row's norm infinite: itself a NaN, the rest zeros; opposite infinities, as
+    any NaN, make the whole row NaN; finite rows are not touched by it.  Scales stay finite."""
+    import nvfp4_block_scaled_mm_b200 as L
+    x, r, w = randn(T, H, dtype=dt, seed=1), randn(T, H, dtype=dt, seed=2), torch.ones(H, dtype=dt)
+    x0, r0 = x.clone(), r.clone()
+    x[1, 7] = float("inf")
+    r[2, H - 1] = float("-inf")
+    x[4, 3], r[4, 3] = float("inf"), float("-inf")
+    out = [torch.empty(T, H, dtype=dt, device=DEV) for _ in range(2)]
+    rd, rd0 = r.to(DEV), r0.to(DEV)
+    q, s = L.add_rmsnorm_fp8_quantize(x.to(DEV), w.to(DEV), rd, norm_out=out[0])
+    q0, s0 = L.add_rmsnorm_fp8_quantize(x0.to(DEV), w.to(DEV), rd0, norm_out=out[1])
+    same = [i for i in range(T) if i not in (1, 2, 4)]
+    assert torch.equal(q.view(torch.uint8)[same], q0.view(torch.uint8)[same]) and torch.equal(s[same], s0[same])
+    assert torch.equal(out[0][same], out[1][same])
+    assert torch.isfinite(s).all()
+    for i, j in ((1, 7), (2, H - 1)):
+        for got in (q[i].float(), out[0][i].float()):
+            assert torch.isnan(got[j]) and torch.all(torch.cat([got[:j], got[j + 1:]]) == 0)
+    assert torch.isnan(q[4].float()).all() and torch.isnan(out[0][4]).all()
+    assert torch.isposinf(rd[1, 7]) and torch.isneginf(rd[2, H - 1]) and torch.isnan(rd[4, 3])
+
+
+def test_norm_of_rows_whose_squares_pass_fp32():
+    """Documented: the mean square is held in fp32, and a row for which it overflows gives zeros."""
+    import nvfp4_block_scaled_mm_b200 as L
+    x = torch.full((3, 256), 1.0, device=DEV)
+    x[1] = 1e20
+    x[2] = 1e18
+    q, s = L.add_rmsnorm_fp8_quantize(x, torch.ones(256, device=DEV))
+    assert torch.all(q[1].float() == 0) and torch.all(q[0].float() == 448) and torch.all(q[2].float() == 448)
+    assert torch.isfinite(s).all()
