@@ -738,21 +738,38 @@ def _refuse_gradient_in_capture(name: str) -> None:
                          f"{name}_backward inside the capture")
 
 
-def _refuse_gradients(name: str, **tensors) -> None:
+def _refuse_gradients(call: str, names: str, *tensors) -> None:
     """A call that records no graph refuses tensors that ask for one (None: not given): its results would lose their
-    gradients without an error.  Under torch.no_grad() nothing is asked for."""
+    gradients without an error.  Under torch.no_grad() nothing is asked for.  `names`: the tensors', for the message."""
     if torch.is_grad_enabled():
-        for key, t in tensors.items():
+        for t in tensors:
             if t is not None and t.requires_grad:
-                raise ValueError(f"{name} records no gradient and {key} requires one: detach it, or call under torch.no_grad()")
-    _refuse_tangents(name, **tensors)
+                key = next(k for k, u in zip(names.split(), tensors) if u is t)
+                raise ValueError(f"{call} records no gradient and {key} requires one: detach it, or call under torch.no_grad()")
+    if forward_ad._current_level >= 0:
+        _refuse_tangents(call, names, *tensors)
 
 
-def _refuse_tangents(name: str, **tensors) -> None:
-    if forward_ad._current_level >= 0:             # inside a forward-mode context
-        for key, t in tensors.items():
-            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-                raise ValueError(f"{name} has no forward-mode derivative and {key} carries a tangent")
+def _plain_operands(call: str, anchor_name: str, anchor: torch.Tensor, **others) -> None:
+    """:func:`_same_device` and :func:`_refuse_gradients` of a call's tensors, in one pass over them."""
+    device, asks = anchor.device, torch.is_grad_enabled()
+    if asks and anchor.requires_grad:
+        _refuse_gradients(call, anchor_name, anchor)
+    for name, t in others.items():
+        if t is not None:
+            if t.device != device:
+                _same_device(anchor_name, anchor, **{name: t})
+            if asks and t.requires_grad:
+                _refuse_gradients(call, name, t)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents(call, " ".join((anchor_name, *others)), anchor, *others.values())
+
+
+def _refuse_tangents(call: str, names: str, *tensors) -> None:
+    """Inside a forward-mode context (forward_ad._current_level >= 0)."""
+    for key, t in zip(names.split(), tensors):
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{call} has no forward-mode derivative and {key} carries a tangent")
 
 
 class _MoePermuteFn(torch.autograd.Function):
@@ -804,7 +821,8 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
         raise ValueError(f"num_experts = {E}, align = {align}: 1 <= num_experts <= 1024 and 1 <= align <= 4096 are required")
     capacity = moe_capacity(T, top_k, E, align)
     _same_device("x", x, topk_ids=topk_ids, out=out)
-    _refuse_tangents("moe_permute", x=x)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("moe_permute", "x", x)
     if x.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out is not supported for an x that requires gradients")
@@ -818,9 +836,10 @@ def moe_permute(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int, *, al
         _need(out, "out", x.dtype, 2)
         if out.shape[0] < capacity or out.shape[1] != x.shape[1]:
             raise ValueError(f"out must be [capacity, H] with capacity >= {capacity} and H = {x.shape[1]}, got {tuple(out.shape)}")
-        _refuse_gradients("moe_permute into a given buffer", out=out)
+        _refuse_gradients("moe_permute into a given buffer", "out", out)
     permutation = MoePermutation(*_moe_permute(x, topk_ids, E, align, zero_padding, out))
-    _written(given)
+    if given is not None:
+        increment_version(given)
     return permutation
 
 
@@ -829,7 +848,7 @@ def moe_permute_backward(grad_rows: torch.Tensor, expanded_idx_to_permuted_idx: 
     """Gradient of :func:`moe_permute` by x: ``grad_x[t] = sum_j grad_rows[idx[t, j]]`` over the active
     slots, in fp32 in slot order, rounded once.  Not differentiable itself."""
     if isinstance(grad_rows, torch.Tensor):
-        _refuse_gradients("moe_permute_backward", grad_rows=grad_rows)
+        _refuse_gradients("moe_permute_backward", "grad_rows", grad_rows)
     return _moe_unpermute(grad_rows, expanded_idx_to_permuted_idx, None, out, "grad_rows")
 
 
@@ -850,11 +869,12 @@ def _moe_unpermute(y, idx, topk_weights, out, name="y"):
         _need(out, "out", y.dtype, 2)
         if out.shape != (T, H):
             raise ValueError(f"out must be [T, H] = [{T}, {H}], got {tuple(out.shape)}")
-        _refuse_gradients("a sum into a given buffer", out=out)
+        _refuse_gradients("a sum into a given buffer", "out", out)
     _same_device(name, y, expanded_idx_to_permuted_idx=idx, topk_weights=topk_weights, out=out)
     _call(_lib.nvfp4lora_moe_unpermute, y.device, y.data_ptr(), y.shape[0], H, _ROW_DTYPES[y.dtype], idx.data_ptr(),
           None if topk_weights is None else topk_weights.data_ptr(), T, top_k, out.data_ptr())
-    _written(given)
+    if given is not None:
+        increment_version(given)
     return out
 
 
@@ -890,8 +910,8 @@ def moe_unpermute(y: torch.Tensor, permutation, topk_weights: Optional[torch.Ten
     :func:`moe_unpermute_backward`, needs the tables); as for :func:`moe_permute`, not while a CUDA
     graph is captured and not in forward mode.
     """
-    if isinstance(y, torch.Tensor):
-        _refuse_tangents("moe_unpermute", y=y, topk_weights=topk_weights)
+    if forward_ad._current_level >= 0 and isinstance(y, torch.Tensor):
+        _refuse_tangents("moe_unpermute", "y topk_weights", y, topk_weights)
     whole = isinstance(permutation, MoePermutation)
     idx = permutation.expanded_idx_to_permuted_idx if whole else permutation
     if torch.is_grad_enabled() and (getattr(y, "requires_grad", False) or getattr(topk_weights, "requires_grad", False)):
@@ -942,15 +962,17 @@ def moe_unpermute_backward(grad_out: torch.Tensor, y: Optional[torch.Tensor], ex
         _need(grad_rows, "grad_rows", grad_out.dtype, 2)
         if grad_rows.shape != (rows, H):
             raise ValueError(f"grad_rows must be [rows, H] = [{rows}, {H}], got {tuple(grad_rows.shape)}")
-    _refuse_gradients("moe_unpermute_backward", grad_out=grad_out, grad_rows=given)
-    _refuse_tangents("moe_unpermute_backward", y=y, topk_weights=topk_weights)
+    _refuse_gradients("moe_unpermute_backward", "grad_out grad_rows", grad_out, given)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents("moe_unpermute_backward", "y topk_weights", y, topk_weights)
     _same_device("grad_out", grad_out, y=y, expanded_idx_to_permuted_idx=idx, permuted_idx_to_expanded_idx=inv,
                  m_indptr=m_indptr, topk_weights=topk_weights, grad_rows=grad_rows)
     _call(_lib.nvfp4lora_moe_unpermute_backward, grad_out.device, grad_out.data_ptr(),
           None if topk_weights is None else y.data_ptr(), rows, H, _ROW_DTYPES[grad_out.dtype], idx.data_ptr(),
           inv.data_ptr(), m_indptr.data_ptr(), m_indptr.shape[0] - 1, _ptr(topk_weights), T, top_k,
           grad_rows.data_ptr(), _ptr(grad_weights))
-    _written(given)
+    if given is not None:
+        increment_version(given)
     return grad_rows, grad_weights
 
 
@@ -991,15 +1013,15 @@ def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, q: Optional[torch.Tens
     _need(x, "x", x.dtype, 2)
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows = {block_rows}: 1 or 128 is required")
-    given = q, scales
+    given = (q, scales) if q is not None or scales is not None else None
     q, scales = _fp8_outputs(x, block_rows, q, scales)
-    _same_device("x", x, q=q, scales=scales)
-    _refuse_gradients("fp8_quantize", x=x, q=q, scales=scales)
+    _plain_operands("fp8_quantize", "x", x, q=q, scales=scales)
     rows, H = x.shape
     sr, sg = scales.stride()
     _call(_lib.nvfp4lora_fp8_quantize, x.device, x.data_ptr(), rows, H, _ROW_DTYPES[x.dtype], block_rows, q.data_ptr(),
           scales.data_ptr(), sr, sg)
-    _written(*given)
+    if given is not None:
+        _written(*given)
     return q, scales
 
 
@@ -1026,14 +1048,14 @@ def add_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
             _need(t, name, x.dtype, 2)
             if t.shape != x.shape:
                 raise ValueError(f"{name} must be [rows, H] = {tuple(x.shape)}, got {tuple(t.shape)}")
-    given = residual, norm_out, q, scales
+    given = [t for t in (residual, norm_out, q, scales) if t is not None]
     q, scales = _fp8_outputs(x, 1, q, scales)
-    _same_device("x", x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
-    _refuse_gradients("add_rmsnorm_fp8_quantize", x=x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
+    _plain_operands("add_rmsnorm_fp8_quantize", "x", x, weight=weight, residual=residual, norm_out=norm_out, q=q, scales=scales)
     sr, sg = scales.stride()
     _call(_lib.nvfp4lora_rmsnorm_fp8_quantize, x.device, x.data_ptr(), _ptr(residual), weight.data_ptr(), x.shape[0], H,
           _ROW_DTYPES[x.dtype], eps, _ptr(norm_out), q.data_ptr(), scales.data_ptr(), sr, sg)
-    _written(*given)
+    if given:
+        increment_version(given)
     return q, scales
 
 
@@ -1076,10 +1098,10 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
         _need(out, "out", out_dtype, 2)
         if out.shape != (M, N):
             raise ValueError(f"out must be [M, N] = [{M}, {N}]")
-    _same_device("a", a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
-    _refuse_gradients("mm_fp8", a=a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
+    _plain_operands("mm_fp8", "a", a, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
     sm, sk = a_scale.stride()
     _call(_lib.nvfp4lora_mm_fp8, a.device, a.data_ptr(), b.data_ptr(), a_scale.data_ptr(), sm, sk, b_scale.data_ptr(),
           _ptr(bias), out.data_ptr(), _ROW_DTYPES[out_dtype], M, N, K)
-    _written(given)
+    if given is not None:
+        increment_version(given)
     return out

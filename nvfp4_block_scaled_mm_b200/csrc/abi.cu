@@ -726,7 +726,8 @@ bool overlap_elements(const void* p, int64_t np, const float* base, int64_t ni, 
     };
     const Wide inner = 4 * ((Wide)(nj - 1) * sj + 1);
     Wide first = 0, last = 0;
-    if (ni > 1 && 4 * (Wide)si < inner) return lo < inner + 4 * (Wide)(ni - 1) * si && hi > 0;
+    if (lo >= inner + 4 * (Wide)(ni - 1) * si || hi <= 0) return false;
+    if (ni > 1 && 4 * (Wide)si < inner) return true;
     if (!pieces(ni, 4 * (Wide)si, inner, first, last)) return false;
     if (first < last) return true;               // two rows' bytes: the second's first element lies between
     lo -= first * 4 * si;
