@@ -407,7 +407,8 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_rmsnorm_fp8_quantize(
  *   bias    bf16 [N] or NULL, added in fp32 before the single rounding.
  *   out     out_dtype (bf16, fp16 or fp32) [M, N] row-major, aligned to its elements, no byte of an operand, of
  *           the scales' elements or of bias among its own.
- * Sums are held in fp32.  Rules: M >= 1, N >= 1, K >= 16 with K % 16 == 0 (K <= 2^20); a and b 16-byte
+ * Sums are held in fp32; the order of the K blocks depends on the shape and on the element's tile (a repeated call
+ * gives the same bits, equal rows in different places may not).  Rules: M >= 1, N >= 1, K >= 16 with K % 16 == 0 (K <= 2^20); a and b 16-byte
  * aligned.  The last K block and the last 128 rows of b may be partial.  The pages have no counterpart.
  */
 NVFP4LORA_API nvfp4lora_status nvfp4lora_mm_fp8(

@@ -1067,7 +1067,9 @@ def mm_fp8(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: tor
 
     a: float8_e4m3fn ``[M, K]``; b: float8_e4m3fn ``[N, K]``; a_scale: fp32 ``[M, ceil(K / 128)]`` of any
     strides (column-major, as :func:`fp8_quantize` makes it, is read fastest); b_scale: fp32
-    ``[ceil(N / 128), ceil(K / 128)]`` contiguous; bias: bf16 ``[N]``; out overlaps none of them.  K % 16 == 0; any M, N >= 1.  As for
+    ``[ceil(N / 128), ceil(K / 128)]`` contiguous; bias: bf16 ``[N]``; out overlaps none of them.  K % 16 == 0; any M, N >= 1.  A
+    repeated call gives the same bits; the order in which a row's K blocks are added depends on the shape and on the row's
+    place, so equal rows in different places may differ by the rounding of their fp32 sums.  As for
     :func:`mm_nvfp4_lora`, out is defined once a later :func:`nvfp4lora_device_status` has returned
     without raising ``DeviceTimeoutError``.  Not differentiable: a tensor that requires gradients is refused
     outside ``torch.no_grad()``."""

@@ -908,10 +908,13 @@ struct Fp8Plan {
 // clusters of those sizes fill the GPU's processor clusters badly) while all CTAs are resident at once (a
 // second wave always lost: 64 x 8192 x 4096 12.2 us with 4-way clusters, 19.4 with 5) and either SMs are free or
 // a CTA still has 16 blocks to stream (16 x 4096 x 4096: 7.0 us 4-way, 7.4 8-way; 16 x 4096 x 14336: 14.3 and 13.2).
-// With 128-token tiles the SM-pair kernel takes what cannot be split (300 x 4096 x 4096: 14.6 us against 20.3), and
-// what can be split only 2-way over fewer than 48 blocks: its time per block of K is the lower, 2-way splits halve
-// the blocks (256 x 4096 x 4096: 14.0 us against 15.5 2-way; x 14336: 39.1 against 34.5; 128 x 4096 x 4096, 4-way:
-// 13.9 against 11.7).  Its tiles are 128 columns wide while they fit the GPU in one wave (512 x 4096 x 4096: 14.8 us
+// With 128-token tiles the SM-pair kernel takes what cannot be split (300 x 4096 x 4096: 13.7 us against 19.6 unsplit;
+// N x 8192 with N = 10240: 65 rows 32.2 against 33.7, 128 32.9 and 35.3, 256 33.4 and 69; N = 28672: 60.9 and 70, 63
+// and 74, 67 and 150), and what can be split only 2-way over fewer than 48 blocks: its time per block of K is the lower,
+// 2-way splits halve the blocks.  Pair against 2-way over 16, 32, 48, 64 and 112 blocks: 128 x 5120 9.0 and 11.2, 13.9
+// and 15.2, 18.8 and 18.9, 23.7 and 22.6, 38.2 and 34.3 us; 128 x 9472 9.8 and 12.0, 14.7 and 15.9, 19.6 and 19.7, 24.9
+// and 24.0, 40.9 and 37.9; 256 x 4096 8.7 and 11.4, 13.4 and 15.1, 18.0 and 18.7, 22.6 and 22.4, 36.5 and 33.6.  (128 x
+// 4096 x 4096, 4-way: 13.9 on the pair against 11.7.)  Its tiles are 128 columns wide while they fit the GPU in one wave (512 x 4096 x 4096: 14.8 us
 // against 19.6 with 256; 1536 x 2048 x 4096, 96 tiles of 128: 25.7 against 21.0).
 Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t kblocks, int sms) {
     Fp8Plan p{false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1, 256};

@@ -16,13 +16,14 @@
 // warps of each CTA read the previous one (128 lanes x 256 columns: one warp per lane quarter and 128
 // columns, which see a single sb per K block).  Registers are split by warpgroup: the promotion warps
 // hold 128 fp32 sums each and read 16 columns at a time (with 32 the loop spilled: 2.2 ms against 1.5 at
-// 8192 x 28672 x 8192).
+// 8192 x 28672 x 8192; 16 bytes of spills per thread are left with 16-bit outputs).
 // With few tiles (TN = 128) a tile is 256 x 128, so that twice as many SM pairs work: four products of 128 columns in
 // TMEM, 64 columns per promotion warp, no register split.
 // What bounds it: the promotion, not the tensor pipe.  A K block takes about 850 cycles without operand loads and
 // 950 to 1100 with them, against 512 of MMAs: a promotion warp needs about 410 for its 128 columns, 185 to see a
-// product that is ready and 260 for the rest of its loop.  8192 x 28672 x 8192 runs 1.55 to 1.65 ms in short
-// runs (2.3 to 2.5 PFLOP/s, 0.68 to 0.72 of twice the measured bf16 rate).  Products of 128 columns (four in TMEM) with two
+// product that is ready and 260 for the rest of its loop (the last two are latency, not a limit).  8192 x 28672 x 8192
+// runs 1.55 to 1.68 ms in short runs (2.3 to 2.5 PFLOP/s, 0.67 to 0.72 of twice the measured bf16 rate) and 1.88 to
+// 1.90 back to back (0.59 to 0.60), under the power limit.  Products of 128 columns (four in TMEM) with two
 // issuers, sixteen promotion warps of 64 columns, scales staged by a warp of their own and scales loaded two to four
 // blocks ahead all measured level or slower.
 #pragma once
@@ -206,7 +207,7 @@ __device__ __forceinline__ void fp8_tile(int tile, int m_tiles, int n_tiles, int
 __device__ __forceinline__ int fp8_box_at(int r, int at) { return r * 64 + (at ^ ((r >> 1 & 3) << 4)); }
 
 // The part of a box that lies in out (rows x cols elements from `out` on), a vector V of its rows' alignment per lane
-// (6606 x 21984 x 1472: 236 us with TMA stores; 280 with 4 bytes per lane at N = 21986, 359 with 2 at 21987;
+// (6606 x 21984 x 1472: 233 us with TMA stores; 278 to 328 with 4 bytes per lane at N = 21986, 359 to 380 with 2 at 21987;
 // 300 x 4100 x 4112, 8 bytes: 15.1 us, 16.9 with one element per lane).
 template <typename V, typename E>
 __device__ __forceinline__ void fp8_store_box(const uint8_t* box, E* out, int64_t N, int rows, int cols, int lane) {
@@ -220,7 +221,9 @@ __device__ __forceinline__ void fp8_store_box(const uint8_t* box, E* out, int64_
 
 // The K block that a tile starts with; it goes on around the end.  Tiles that run at one time and share an operand
 // would otherwise all read the same lines of it at the same time, from a few L2 slices (256 x 8192 x 8192: 37 us
-// with every tile from block 0, 30 with this; 300 x 4100 x 4112: 19.6 and 17.1; large products are level).
+// with every tile from block 0, 30 with this; 300 x 4100 x 4112: 19.6 and 17.1; large products are level).  The order
+// of an element's sum so depends on its tile: equal rows of a in different row tiles may differ in their last bits, while
+// a repeated call gives the same bits.
 __device__ __forceinline__ int fp8_first_block(int m_blk, int n_blk, int kblocks) {
     return (int)((3u * (uint32_t)n_blk + (uint32_t)m_blk) % (uint32_t)kblocks);
 }

@@ -13,9 +13,11 @@
 // make rms zero: zeros, and a NaN in an infinity's place.
 //
 // HBM-bound: the norm of 8192 x 8192 bf16 with residual and the normed rows kept runs 92 us (6.6 TB/s), of 65536 x 512
-// 36 us (6.5); without either, where it moves 3 bytes per element, it is bound by instruction issue (46 us, 4.4).
+// 36 us (6.5); without either, where it moves 3 bytes per element, 45 us (4.5), at two thirds of the issue slots and of the
+// copy rate: a row's loads, the barrier and the arithmetic follow each other within a CTA.
 // The quantizer of 8192 x 8192 takes 32 us by rows (6.3) and of 28672 x 8192 102 us by blocks (6.9, part of the
-// writes still in L2).  Sixteen rows take 2 us, launch latency.
+// writes still in L2).  Sixteen rows take 2 us, launch latency.  Rows off 16 bytes take element accesses: the norm of 883 x
+// 5804 14.7 us (6.3 at 5808), the quantizer of 11805 x 4570 53 (27 at 4576).
 #pragma once
 
 #include <cstdint>
@@ -152,7 +154,7 @@ rmsnorm_fp8_kernel(const Fp8QuantArgs a) {
     void* res = a.residual != nullptr ? row_at<TY>(a.residual, row, H) : nullptr;
     float h[NV][8];
     // rows of four chunks per warp load the weight after the sum: held across it, it would spill at the 64
-    // registers of two CTAs of 512 threads
+    // registers of two CTAs of 512 threads (fp32 rows spill 60 bytes as it is)
     constexpr bool kLate = NV == 4;
     typename C::Raw wt[kLate ? 1 : NV];
     grid_dependency_wait();

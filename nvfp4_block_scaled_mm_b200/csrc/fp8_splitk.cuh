@@ -13,6 +13,7 @@
 //   * the S partial sums meet in distributed shared memory: CTA r reads every CTA's sums of the token
 //     columns [MT r / S, MT (r + 1) / S), adds them in rank order and rounds once, so the result does
 //     not depend on the schedule.
+// 80 registers at two CTAs per SM; with MT = 64 a thread spills 4 bytes.
 // Bound by streaming the weights from HBM where there are many: 16 x 28672 x 8192 runs 40 us (5.9 TB/s of the
 // measured 6.46).  At 16 x 4096 x 4096 (17 MB, 6.9 us) the stream itself takes 2.7 us at that rate; the rest is the
 // first load's latency (0.9 us), the meeting of the partial sums (1.4 us) and the start and end of the grid.
