@@ -353,8 +353,8 @@ NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_permute_backward(
  *     grad_weights[t, j]   = sum_h grad_out[t, h] * y[row(t, j), h] (fp32; 0 for an inactive slot)
  * Padding rows of the segments get zeros; rows from m_indptr[num_experts] on are left as they were.
  * The tables are those that nvfp4lora_moe_permute wrote.  topk_weights and grad_weights may both be
- * NULL (weights 1; y is then not read and may be NULL).  grad_rows may be y itself; otherwise grad_rows and
- * grad_weights share no byte with an input or each other.  Rules as for nvfp4lora_moe_unpermute.
+ * NULL (weights 1; y is then not read and may be NULL).  grad_rows may be y itself and
+ * grad_weights topk_weights itself; otherwise the two share no byte with an input or each other.  Rules as for nvfp4lora_moe_unpermute.
  */
 NVFP4LORA_API nvfp4lora_status nvfp4lora_moe_unpermute_backward(
     const void* grad_out, const void* y, int64_t padded_rows, int64_t H, int32_t dtype,

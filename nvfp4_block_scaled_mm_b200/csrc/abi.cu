@@ -1463,13 +1463,15 @@ nvfp4lora_status nvfp4lora_moe_unpermute_backward(const void* grad_out, const vo
     if (!aligned(grad_out, es) || !aligned(y, es) || !aligned(grad_rows, es) || !aligned(expanded_idx_to_permuted_idx, 4) ||
         !aligned(permuted_idx_to_expanded_idx, 4) || !aligned(topk_weights, 4) || !aligned(grad_weights, 4))
         return fail(NVFP4LORA_ERR_INVALID_ARG, "rows must be aligned to their elements, the tables 4-byte aligned");
-    // grad_rows may be y itself: a thread reads its elements before it writes them
+    // grad_rows may be y itself, grad_weights topk_weights: a thread reads its elements, and a block a token's weights,
+    // before they are written
     const int64_t bytes = padded_rows * H * es, n = num_tokens * top_k;
     if ((st = check_apart({{"grad_rows", grad_rows, bytes}, {"grad_weights", grad_weights, n * 4}},
                           {{"grad_out", grad_out, num_tokens * H * es}, {"y", topk_weights && y != grad_rows ? y : nullptr, bytes},
                            {"expanded_idx_to_permuted_idx", expanded_idx_to_permuted_idx, n * 4},
                            {"permuted_idx_to_expanded_idx", permuted_idx_to_expanded_idx, padded_rows * 4},
-                           {"m_indptr", m_indptr, (num_experts + 1) * 4}, {"topk_weights", topk_weights, n * 4}})) != NVFP4LORA_OK)
+                           {"m_indptr", m_indptr, (num_experts + 1) * 4},
+                           {"topk_weights", topk_weights == grad_weights ? nullptr : topk_weights, n * 4}})) != NVFP4LORA_OK)
         return st;
     int dev = 0;
     DeviceInfo* info = nullptr;

@@ -62,3 +62,17 @@ def test_8_bit_calls(side):
                      (res, want_res), (norm, want_norm), (out, want)):
         assert torch.equal(got, ref)
     L.nvfp4lora_device_status()
+
+
+def test_gradient_of_the_weights_in_their_place():
+    """grad_weights may be topk_weights itself: every slot's weight is read before its gradient is written."""
+    for T, k, H in ((50, 16, 96), (700, 7, 2056)):
+        E, g = 6, torch.Generator().manual_seed(T)
+        ids = torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32).to(DEV)
+        x, w = torch.randn(T, H, generator=g).to(BF).to(DEV), torch.rand(T, k, generator=g).to(DEV)
+        p = L.moe_permute(x, ids, E)
+        zeros = torch.zeros_like(p.rows)
+        gy, gw = L.moe_unpermute_backward(x, p.rows, *p[2:], p.m_indptr, w, grad_rows=zeros.clone())
+        L.nvfp4lora_moe_unpermute_backward(x, p.rows, p.rows.shape[0], H, 0, *p[2:], p.m_indptr, E, w, T, k, zeros, w)
+        assert torch.equal(zeros, gy) and torch.equal(w, gw)
+    L.nvfp4lora_device_status()

@@ -296,7 +296,7 @@ def test_unpermute_refuses_overlapping_tables(lib, bad):
 
 @pytest.mark.parametrize("bad", [
     dict(idx=0x17FFFC), dict(inv=0x170000), dict(indptr=0x17FFFC), dict(w=0x170000), dict(gw=0x17FFFC), dict(gw=0x130000),
-    dict(gw=0x1407FC), dict(gw=0x150010), dict(gw=0x160000), dict(gw=0x1031FC), dict(gw=0x11FFFC), dict(y=0x170000, gw=0x17FFFC),
+    dict(gw=0x1407FC), dict(gw=0x150010), dict(gw=0x160004), dict(gw=0x1031FC), dict(gw=0x11FFFC), dict(y=0x170000, gw=0x17FFFC),
     dict(gw=None, w=None, indptr=0x170000),
 ])
 def test_unpermute_backward_refuses_overlapping_tables(lib, bad):
@@ -309,6 +309,6 @@ def test_routed_calls_take_buffers_side_by_side(lib):
                                                 dict(T=100, ws=0x160000, ws_bytes=0x800))),       # a workspace that is not used
             (lib.nvfp4lora_moe_unpermute, UNPERMUTE, (dict(), dict(w=None), dict(idx=0x43200), dict(w=0x20000))),
             (lib.nvfp4lora_moe_unpermute_backward, GRADS, (dict(), dict(y=0x170000), dict(gw=None, w=None), dict(gw=None, w=None, y=0x170010),
-                                                           dict(gw=0x150014), dict(gw=0x180000), dict(y=0x180000)))):
+                                                           dict(gw=0x150014), dict(gw=0x160000), dict(gw=0x180000), dict(y=0x180000)))):
         for ok in oks:
             assert passes_the_host(f, base, ok), (ok, lib.nvfp4lora_last_error())
